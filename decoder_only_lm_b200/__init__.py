@@ -96,6 +96,12 @@ SIGNATURES = {
     "gpt2_matmul": (_i, [_P, _i, _i64, _P, _i, _i64, _i, _i, _i, _i, _f, _i, _P, _i, _i64, _P,
                          _sz, _P]),
     "gpt2_linear": (_i, [_i, _P, _P, _i, _P, _P, _P, _P, _i, _i, _i, _i, _P, _sz, _P]),
+    "gpt2_tree_attention_workspace": (_i, [_i, _i, _i, _i, _i, _i, C.POINTER(_sz)]),
+    "gpt2_tree_attention": (_i, [_P, _i64, _P, _P, _P, _P, _P, _i, _i, _i, _i, _i, _i, _i, _P, _i64,
+                                 _P, _P, _sz, _P]),
+    "gpt2_tree_verify": (_i, [_P, _i64, _P, _i64, _P, _P, _P, _P, _i, _i, _i, _f, _i, _f, _P, _P,
+                              _P, _P]),
+    "gpt2_kv_append": (_i, [_P, _i64, _P, _P, _P, _i, _i, _i, _i, _i, _i, _i, _i, _P, _P, _P, _P]),
     "gpt2_device_error": (_i, [C.POINTER(_i)]),
     "gpt2_launch_count": (_i, [C.POINTER(_i64)]),
     "gpt2_wait_selfcheck": (_i, [C.POINTER(_i)]),
@@ -595,6 +601,179 @@ def sample(logits, vocab, temperature=0.8, top_k=0, top_p=0.9, uniform=None, out
                            _ptr(u), _ptr(out), out.stride(0) if out.dim() > 1 else 1,
                            _stream_ptr(stream)))
     return out
+
+
+# ------------------------------------------------------- decoding with drafted tokens
+def _on_device_of(t, stream):
+    """Context in which a call on the tensors of t's device runs: that device
+    current, and the caller's stream current (None: the device's current one),
+    so that outputs and workspaces are allocated on the stream that uses them."""
+    import contextlib
+
+    import torch
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _arg(name, t, dtype, shape, device, optional=False):
+    """Checks one dense tensor argument."""
+    if t is None and optional:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _node_rows(name, qkv, dims, H, Hkv, D):
+    """Row stride of activations [..., N, (H + 2 Hkv) D] whose rows are evenly
+    spaced over all leading dimensions."""
+    if qkv.dim() != dims or not qkv.is_cuda or qkv.shape[-1] != (H + 2 * Hkv) * D:
+        raise ValueError(f"{name}: needs a cuda tensor of {dims} dimensions, the last one "
+                         f"(n_head + 2 n_kv_head) * head size = {(H + 2 * Hkv) * D}, got "
+                         f"{tuple(qkv.shape)} on {qkv.device}")
+    ld = qkv.shape[-1]
+    for d in range(dims - 2, -1, -1):  # the spacing given by the innermost dimension that has one
+        if qkv.shape[d] > 1:
+            rows = 1
+            for e in range(d + 1, dims - 1):
+                rows *= qkv.shape[e]
+            ld = qkv.stride(d) // rows
+            break
+    want = ld
+    for d in range(dims - 2, -1, -1):
+        if qkv.shape[d] > 1 and qkv.stride(d) != want:
+            raise ValueError(f"{name}: rows must be evenly spaced, got strides {qkv.stride()}")
+        want *= qkv.shape[d]
+    if qkv.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    return ld
+
+
+def _act_type(name, t):
+    import torch
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: float32 or bfloat16, got {t.dtype}")
+
+
+def tree_attention(qkv, k_cache, v_cache, lens, n_head, parent=None, counts=None, out=None,
+                   lse=None, stream=None):
+    """Attention of drafted nodes over a key/value cache (gpt2_tree_attention).
+
+    qkv: [B, N, (n_head + 2 n_kv_head) D] activations of the nodes (q | k | v;
+    a view with evenly spaced rows will do); k_cache, v_cache: [B, n_kv_head,
+    Tc, D]; lens: int32 [B] cached positions; parent: int32 [B, N], the node
+    before each node, -1 for one that follows the cache (None: a chain, the
+    causal chunk; N = 1: single-token decoding); counts: int32 [B] real nodes of
+    each sequence (None: all).  Returns (out [B, N, n_head D], lse fp32
+    [B, n_head, N]); rows of nodes beyond counts are left as they were (0 in
+    buffers allocated here)."""
+    import torch
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache: needs [B, n_kv_head, Tc, D], got {tuple(k_cache.shape)}")
+    B, Hkv, Tc, D = k_cache.shape
+    _act_type("qkv", qkv)
+    ld = _node_rows("qkv", qkv, 3, n_head, Hkv, D)
+    N, dev = qkv.shape[1], qkv.device
+    if qkv.shape[0] != B:
+        raise ValueError(f"qkv has {qkv.shape[0]} sequences, the cache {B}")
+    _arg("k_cache", k_cache, qkv.dtype, (B, Hkv, Tc, D), dev)
+    _arg("v_cache", v_cache, qkv.dtype, (B, Hkv, Tc, D), dev)
+    _arg("lens", lens, torch.int32, (B,), dev)
+    _arg("parent", parent, torch.int32, (B, N), dev, optional=True)
+    _arg("counts", counts, torch.int32, (B,), dev, optional=True)
+    _arg("out", out, qkv.dtype, (B, N, n_head * D), dev, optional=True)
+    _arg("lse", lse, torch.float32, (B, n_head, N), dev, optional=True)
+    dt = _dtype_code(qkv)
+    ws_b = C.c_size_t()
+    _check(lib.gpt2_tree_attention_workspace(B, N, n_head, Hkv, D, dt, C.byref(ws_b)))
+    with _on_device_of(qkv, stream):
+        new = torch.empty if counts is None else torch.zeros
+        if out is None:
+            out = new((B, N, n_head * D), dtype=qkv.dtype, device=dev)
+        if lse is None:
+            lse = new((B, n_head, N), dtype=torch.float32, device=dev)
+        ws = torch.empty(ws_b.value, dtype=torch.uint8, device=dev)
+        _check(lib.gpt2_tree_attention(_ptr(qkv), ld, _ptr(k_cache), _ptr(v_cache), _ptr(lens),
+                                       _ptr(parent), _ptr(counts), dt, B, N, n_head, Hkv, D, Tc,
+                                       _ptr(out), n_head * D, _ptr(lse), _ptr(ws), ws_b.value,
+                                       _stream_ptr(stream)))
+    return out, lse
+
+
+def tree_verify(logits, vocab, tokens, uniform, temperature=0.8, top_k=0, top_p=0.9, parent=None,
+                draft_logits=None, counts=None, stream=None):
+    """Which drafted tokens are kept, and the token after them (gpt2_tree_verify).
+
+    logits: fp32 [B, N, >= vocab], the target's row of each node (node 0 is the
+    last token already decided); draft_logits: the rows that each node's children
+    were drawn from, or None for guesses; tokens: int32 [B, N]; uniform: fp32
+    [B, N] in [0, 1); parent, counts as in tree_attention.  Returns (path int32
+    [B, N], accepted nodes in order from node 0 and -1 behind them; n_path int32
+    [B]; next int32 [B])."""
+    import torch
+    if logits.dim() != 3 or logits.dtype != torch.float32 or not logits.is_cuda:
+        raise ValueError("logits: needs a float32 cuda tensor [B, N, >= vocab]")
+    B, N, _ = logits.shape
+    dev = logits.device
+
+    def rows(name, t):
+        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[:2] != (B, N) or t.device != dev or \
+                t.shape[2] < vocab or t.stride(2) != 1 or \
+                (B > 1 and N > 1 and t.stride(0) != N * t.stride(1)):
+            raise ValueError(f"{name}: needs float32 rows [B, N, >= vocab], evenly spaced, got "
+                             f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+        return t.stride(1) if N > 1 else t.stride(0) if B > 1 else t.shape[2]
+
+    ld = rows("logits", logits)
+    ld_draft = 0 if draft_logits is None else rows("draft_logits", draft_logits)
+    _arg("tokens", tokens, torch.int32, (B, N), dev)
+    _arg("uniform", uniform, torch.float32, (B, N), dev)
+    _arg("parent", parent, torch.int32, (B, N), dev, optional=True)
+    _arg("counts", counts, torch.int32, (B,), dev, optional=True)
+    with _on_device_of(logits, stream):
+        path = torch.empty((B, N), dtype=torch.int32, device=dev)
+        n_path = torch.empty(B, dtype=torch.int32, device=dev)
+        nxt = torch.empty(B, dtype=torch.int32, device=dev)
+        _check(lib.gpt2_tree_verify(_ptr(logits), ld, _ptr(draft_logits), ld_draft, _ptr(tokens),
+                                    _ptr(parent), _ptr(counts), _ptr(uniform), B, N, vocab,
+                                    temperature, top_k, top_p, _ptr(path), _ptr(n_path), _ptr(nxt),
+                                    _stream_ptr(stream)))
+    return path, n_path, nxt
+
+
+def kv_append(qkv, k_cache, v_cache, lens, path=None, n_path=None, stream=None):
+    """Keys and values of nodes stored into the caches of every layer
+    (gpt2_kv_append): qkv [n_layer, B, N, (n_head + 2 n_kv_head) D] (evenly
+    spaced rows), k_cache, v_cache [n_layer, B, n_kv_head, Tc, D] (changed in
+    place), lens int32 [B]; path, n_path as tree_verify returns them (None: the
+    nodes in order, all of them).  Returns the new lengths, int32 [B]."""
+    import torch
+    if k_cache.dim() != 5:
+        raise ValueError(f"k_cache: needs [n_layer, B, n_kv_head, Tc, D], got {tuple(k_cache.shape)}")
+    L, B, Hkv, Tc, D = k_cache.shape
+    _act_type("qkv", qkv)
+    H = qkv.shape[-1] // D - 2 * Hkv
+    ld = _node_rows("qkv", qkv, 4, H, Hkv, D)
+    N, dev = qkv.shape[2], qkv.device
+    if qkv.shape[:2] != (L, B):
+        raise ValueError(f"qkv has {tuple(qkv.shape[:2])} layers and sequences, the cache {(L, B)}")
+    _arg("k_cache", k_cache, qkv.dtype, (L, B, Hkv, Tc, D), dev)
+    _arg("v_cache", v_cache, qkv.dtype, (L, B, Hkv, Tc, D), dev)
+    _arg("lens", lens, torch.int32, (B,), dev)
+    _arg("path", path, torch.int32, (B, N), dev, optional=True)
+    _arg("n_path", n_path, torch.int32, (B,), dev, optional=True)
+    with _on_device_of(qkv, stream):
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        _check(lib.gpt2_kv_append(_ptr(qkv), ld, _ptr(lens), _ptr(path), _ptr(n_path),
+                                  _dtype_code(qkv), L, B, N, H, Hkv, D, Tc, _ptr(k_cache),
+                                  _ptr(v_cache), _ptr(new_lens), _stream_ptr(stream)))
+    return new_lens
 
 
 def cosine_lr(t, max_lr, min_lr, warmup_steps, total_steps):

@@ -14,6 +14,7 @@
 
 #include "attn_internal.h"
 #include "kernels.h"
+#include "tree_internal.h"
 
 using gpt2_internal::set_error;
 
@@ -278,7 +279,7 @@ int gpt2_device_error(int* code) {
   if (cudaMemcpy(&v, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GPT2_ERR_CUDA;
   int z = 0;
   cudaMemcpy(w, &z, sizeof(int), cudaMemcpyHostToDevice);
-  *code = v ? GPT2_ERR_TIMEOUT : GPT2_OK;
+  *code = v == kTreeBadInput ? GPT2_ERR_ARG : v ? GPT2_ERR_TIMEOUT : GPT2_OK;
   return GPT2_OK;
 }
 

@@ -1,0 +1,273 @@
+// Attention of drafted tokens over a key/value cache, CUDA-core kernel: fp32
+// and bf16, head sizes 16, 32, 64 and 128.
+//
+// Source: [ZERO] "GPT training", Attention (softmax(q k^T / sqrt(D)) v over the
+// positions a query may see); [CS336] section 5 (the cache that reuses the
+// history).  The tree form has no counterpart on the pages: node i sees the
+// cached positions and the nodes on its own path to the root.
+//
+// One pass over the keys with the running maximum m and sum l of each row
+// (log2 domain): for a tile of scores s, m' = max(m, max s), p = 2^(s - m'),
+// l' = l 2^(m - m') + sum p, o' = o 2^(m - m') + p v.  All of it in fp32.
+
+#include "tree_attn.cuh"
+
+using namespace tree;
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int MR = 16;  // query rows of a tile
+constexpr int KT = 64;  // keys of a tile
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<bf16>(const bf16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <int D>
+struct Smem {
+  static constexpr int LD = D + 4;   // row stride: 8 rows of float4 hit 32 banks
+  static constexpr int LP = KT + 4;
+  float q[MR * LD];
+  float k[KT * LD];
+  float v[KT * LD];
+  float p[MR * LP];
+  uint32_t mask[kMaxNodes * kMaskWords];
+  int up[kMaxNodes];
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a) {
+  using S = Split<MR, KT>;
+  constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP;
+  constexpr int V4 = D / 4;              // float4 of a row
+  constexpr int NO = (V4 + 7) / 8;       // float4 of the output a thread holds
+  extern __shared__ float4 smem_raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  const int tid = threadIdx.x;
+  const int r = tid >> 3, kk = tid & 7;  // row of the tile, lane of the row
+  asm volatile("griddepcontrol.launch_dependents;");
+  bool bad = false;
+  int64_t total;
+  S::prefix(a, 0, &total, &bad);
+  if (bad && blockIdx.x == 0) atomicExch(a.err, kTreeBadInput);
+  const int64_t run = run_length(total, gridDim.x);
+  int64_t pos = blockIdx.x * run;
+  const int64_t end = min64(total, pos + run);
+  if (pos >= end) return;
+  int64_t first;
+  int b = S::find(a, pos, &first);
+  int mask_of = -1;  // sequence whose masks are in shared memory
+  const float scale = rsqrtf(float(D)) * kLog2e;
+  const T* qkv = static_cast<const T*>(a.qkv);
+
+  while (pos < end) {
+    const SeqDims s = seq_dims(a, b);
+    const int64_t seq_tiles = S::tiles(a, s);
+    if (pos >= first + seq_tiles) {
+      first += seq_tiles;
+      ++b;
+      continue;
+    }
+    // the piece of one segment that falls into this run
+    const int kt = S::key_tiles(s), rts = S::row_tiles(a, s), ct = S::cache_tiles(s);
+    const int seg = int((pos - first) / kt);
+    const int64_t s0 = first + int64_t(seg) * kt;
+    const int hk = seg / rts, rt = seg % rts;
+    const int t0 = int(pos - s0), t1 = int(min64(kt, end - s0));
+    const int rows = min(MR, s.n * a.G - rt * MR);
+    const T* xb = qkv + int64_t(b) * a.N * a.ld_qkv;  // this sequence's nodes
+    __syncthreads();  // the previous piece is done with shared memory
+    for (int e = tid; e < MR * V4; e += kThreads) {
+      const int rr = e / V4, c = e % V4;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rr < rows) {
+        const int gr = rt * MR + rr, node = gr / a.G, h = hk * a.G + gr % a.G;
+        f = load4(xb + int64_t(node) * a.ld_qkv + int64_t(h) * D + c * 4);
+        f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
+      }
+      *reinterpret_cast<float4*>(&sm.q[rr * LD + c * 4]) = f;
+    }
+    if (t1 > ct && mask_of != b) {
+      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, sm.mask, sm.up, a.err);
+      mask_of = b;
+    }
+    const int node = r < rows ? (rt * MR + r) / a.G : 0;
+    float m = -INFINITY, l = 0.f;
+    float4 o[NO];
+#pragma unroll
+    for (int j = 0; j < NO; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+    for (int t = t0; t < t1; ++t) {
+      const bool fresh = t >= ct;  // keys are nodes, not cache rows
+      const int k0 = (fresh ? t - ct : t) * KT;
+      const int nk = min(KT, (fresh ? s.n : s.len) - k0);
+      const T *kp, *vp;
+      int64_t ld;
+      if (fresh) {
+        kp = xb + int64_t(k0) * a.ld_qkv + int64_t(a.H + hk) * D;
+        vp = kp + int64_t(a.Hkv) * D;
+        ld = a.ld_qkv;
+      } else {
+        const int64_t base = ((int64_t(b) * a.Hkv + hk) * a.Tc + k0) * D;
+        kp = static_cast<const T*>(a.k) + base;
+        vp = static_cast<const T*>(a.v) + base;
+        ld = D;
+      }
+      for (int e = tid; e < KT * V4; e += kThreads) {
+        const int row = e / V4, c = e % V4;
+        float4 fk = make_float4(0.f, 0.f, 0.f, 0.f), fv = fk;
+        if (row < nk) {
+          fk = load4(kp + row * ld + c * 4);
+          fv = load4(vp + row * ld + c * 4);
+        }
+        *reinterpret_cast<float4*>(&sm.k[row * LD + c * 4]) = fk;
+        *reinterpret_cast<float4*>(&sm.v[row * LD + c * 4]) = fv;
+      }
+      __syncthreads();
+      if (rows > (r & ~3)) {  // some row of this warp is real
+        float sc[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sc[j] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < V4; ++c) {
+          const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[r * LD + c * 4]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[(kk + 8 * j) * LD + c * 4]);
+            sc[j] = fmaf(q4.x, k4.x, sc[j]);
+            sc[j] = fmaf(q4.y, k4.y, sc[j]);
+            sc[j] = fmaf(q4.z, k4.z, sc[j]);
+            sc[j] = fmaf(q4.w, k4.w, sc[j]);
+          }
+        }
+        float mx = m;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = kk + 8 * j;
+          bool see = key < nk;
+          if (fresh && see) {
+            const int kn = k0 + key;
+            see = (sm.mask[node * kMaskWords + (kn >> 5)] >> (kn & 31)) & 1;
+          }
+          if (!see) sc[j] = -INFINITY;
+          mx = fmaxf(mx, sc[j]);
+        }
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        // a row that has seen nothing yet: every p is 2^(-inf) = 0
+        const float base = mx == -INFINITY ? 0.f : mx;
+        const float alpha = exp2f(m - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float p = exp2f(sc[j] - base);
+          sum += p;
+          sm.p[r * LP + kk + 8 * j] = p;
+        }
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l = fmaf(l, alpha, sum);
+        m = mx;
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          o[j].x *= alpha; o[j].y *= alpha; o[j].z *= alpha; o[j].w *= alpha;
+        }
+        __syncwarp();  // a row's probabilities are written and read by one warp
+        for (int key = 0; key < nk; ++key) {
+          const float p = sm.p[r * LP + key];
+          // a node outside the path may hold anything (0 * inf is not 0)
+          if (fresh && p == 0.f) continue;
+#pragma unroll
+          for (int j = 0; j < NO; ++j) {
+            if (kk + 8 * j < V4) {
+              const float4 v4 =
+                  *reinterpret_cast<const float4*>(&sm.v[key * LD + (kk + 8 * j) * 4]);
+              o[j].x = fmaf(p, v4.x, o[j].x);
+              o[j].y = fmaf(p, v4.y, o[j].y);
+              o[j].z = fmaf(p, v4.z, o[j].z);
+              o[j].w = fmaf(p, v4.w, o[j].w);
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    if (t0 == 0 && t1 == kt) {  // the whole segment: finished here
+      if (r < rows) {
+        const int gr = rt * MR + r, h = hk * a.G + gr % a.G;
+        T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + node) * a.ld_out + int64_t(h) * D;
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+          const int c = (kk + 8 * j) * 4;
+          if (c < D) {
+            out[c] = from_f32<T>(o[j].x * inv);
+            out[c + 1] = from_f32<T>(o[j].y * inv);
+            out[c + 2] = from_f32<T>(o[j].z * inv);
+            out[c + 3] = from_f32<T>(o[j].w * inv);
+          }
+        }
+        if (a.lse && kk == 0)
+          a.lse[(int64_t(b) * a.H + h) * a.N + node] = (m + log2f(l)) * kLn2;
+      }
+    } else {
+      float* w = a.ws + slot_of(blockIdx.x, s0, run) * slot_floats<MR>(D);
+      if (r < rows) {
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+          if (kk + 8 * j < V4) *reinterpret_cast<float4*>(&w[r * D + (kk + 8 * j) * 4]) = o[j];
+        if (kk == 0) {
+          w[MR * D + r] = m;
+          w[MR * D + MR + r] = l;
+        }
+      }
+    }
+    pos = s0 + t1;
+  }
+}
+
+int simt_grid() { return 4 * gpt2_internal::sm_count(); }
+
+template <typename T, int D>
+int launch_simt(const TreeAttnArgs& a, cudaStream_t st) {
+  const int smem = int(sizeof(Smem<D>));
+  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_simt_kernel<T, D>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int grid = simt_grid();
+  tree_attn_simt_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
+  COUNT_LAUNCH(1);
+  GPT2_LAUNCH_CHECK();
+  return launch_combine<T, MR, KT>(a, grid, st);
+}
+
+template <typename T>
+int launch_simt_d(const TreeAttnArgs& a, cudaStream_t st) {
+  switch (a.D) {
+    case 16: return launch_simt<T, 16>(a, st);
+    case 32: return launch_simt<T, 32>(a, st);
+    case 64: return launch_simt<T, 64>(a, st);
+    default: return launch_simt<T, 128>(a, st);
+  }
+}
+
+}  // namespace
+
+size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16_in) {
+  return size_t(2) * simt_grid() * slot_floats<MR>(D) * sizeof(float);
+}
+
+int launch_tree_attn(const TreeAttnArgs& a, int bf16_in, cudaStream_t st) {
+  return bf16_in ? launch_simt_d<bf16>(a, st) : launch_simt_d<float>(a, st);
+}

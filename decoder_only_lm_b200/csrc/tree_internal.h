@@ -1,0 +1,56 @@
+// Decoding with drafted tokens (internal): attention of a tree of drafted
+// tokens over a cache, verification, and the cache store.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+// error-word value of a length, count, parent or path that is out of range
+// (read back as GPT2_ERR_ARG; other values are bounded-wait timeouts)
+constexpr int kTreeBadInput = 0x7A00;
+
+struct TreeAttnArgs {
+  const void* qkv;
+  int64_t ld_qkv;
+  const void *k, *v;
+  const int32_t *lens, *parent, *counts;
+  int B, N, H, Hkv, G, D, Tc;  // G = H / Hkv
+  void* out;
+  int64_t ld_out;
+  float* lse;
+  float* ws;
+  int* err;
+};
+
+size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16);
+int launch_tree_attn(const TreeAttnArgs& a, int bf16, cudaStream_t st);
+
+struct TreeVerifyArgs {
+  const float* logits;
+  int64_t ld;
+  const float* draft;  // nullable
+  int64_t ld_draft;
+  const int32_t *tokens, *parent, *counts;
+  const float* uniform;
+  int B, N, V;
+  float temperature;
+  int top_k;
+  float top_p;
+  int32_t *path, *n_path, *next;
+  int* err;
+};
+constexpr int kTreeMaxNodes = 256;
+constexpr int kTreeMaxVocab = 98304;
+int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st);
+
+struct KvAppendArgs {
+  const void* qkv;
+  int64_t ld_qkv;
+  const int32_t *path, *n_path, *lens;
+  int L, B, N, H, Hkv, D, Tc;
+  void *k, *v;
+  int32_t* new_lens;
+  int* err;
+};
+int launch_kv_append(const KvAppendArgs& a, int elem_bytes, cudaStream_t st);

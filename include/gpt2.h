@@ -518,6 +518,101 @@ int gpt2_linear(int epi, const void* x, const void* w, int w_kn, const float* bi
                 const void* in, void* out, void* out2, int M, int N, int K, int dtype,
                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- drafted tokens
+ * Decoding with drafted tokens: a small model (or any guess) proposes several
+ * next tokens as a tree, the model runs once over all of them, and the tokens
+ * that the target distribution would have produced are kept.  Per step:
+ * gpt2_tree_attention in every layer, gpt2_tree_verify on the logits of the
+ * nodes, gpt2_kv_append of the accepted path.  No counterpart on the pages
+ * beyond the parts named at each call.
+ *
+ * A tree of N nodes (1 <= N <= 256) per sequence: parent[b*N + i] < i is the
+ * node that node i follows, -1 for a node that follows the cached tokens
+ * directly.  parent = NULL stands for the chain parent(i) = i - 1: a chunk of a
+ * prompt, or with N = 1 the single token of ordinary decoding.  counts
+ * (nullable: N each) gives the nodes of sequence b that are real, 0 .. N.
+ * Lengths, counts and trees are read on the device, so a recorded launch
+ * follows their contents.  What is out of range there (a length outside
+ * 0 .. Tc, a count outside 0 .. N, a parent outside -1 .. i-1) is recorded and
+ * read back as GPT2_ERR_ARG by gpt2_device_error; a sequence with a bad length
+ * or count is treated as having no node, a bad parent as -1.
+ *
+ * Caches: [B, Hkv, Tc, D], the row of position t of head hk of sequence b at
+ * ((b Hkv + hk) Tc + t) D, as gpt2_generate_cached keeps them (Hkv = H there).
+ * A node's activations: qkv row (H + 2 Hkv) D elements, q | k | v, head h =
+ * channels [hD, (h+1)D) of its part; query head h reads key/value head
+ * h / (H / Hkv).  Rows of consecutive nodes are ld_qkv elements apart, of
+ * consecutive sequences N ld_qkv.
+ *
+ * Every device pointer 16-byte aligned; ld_qkv a multiple of 16 bytes; D = 16,
+ * 32, 64 or 128; H a multiple of Hkv; dtype GPT2_F32 or GPT2_BF16. */
+
+/* Attention of the nodes over the cache and over each other:
+ *   out[b, i, hD ..] = sum_j p_j v_j,  p = softmax(q_i . k_j / sqrt(D))
+ * over the cached positions j < lens[b] and the nodes on the path from i to the
+ * root, i included [ZERO: Attention; CS336: text generation].  lse (nullable),
+ * fp32 [B, H, N]: log of the softmax's normaliser.  The caches are read only up
+ * to lens[b] and not written; what other nodes or cache rows hold (infinities
+ * and NaN too) does not reach a row.  Rows of nodes i >= counts[b] of out and
+ * lse are left as they were.  out: row (b, i) at (b N + i) ld_out, ld_out >=
+ * H D.  fp32 accumulation and softmax; with GPT2_BF16 the probabilities are
+ * rounded to bf16 for the product with v.  workspace: device memory of at least
+ * gpt2_tree_attention_workspace() bytes, free again when the call's work is
+ * done (calls that may overlap need one each).  Results do not depend on
+ * timing.  Asynchronous on `stream`. */
+int gpt2_tree_attention_workspace(int B, int N, int H, int Hkv, int D, int dtype, size_t* bytes);
+int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, const void* v_cache,
+                        const int32_t* lens, const int32_t* parent, const int32_t* counts,
+                        int dtype, int B, int N, int H, int Hkv, int D, int Tc, void* out,
+                        int64_t ld_out, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Which drafted tokens are kept, and the token after them.  Node 0 is the root:
+ * the last token already decided; nodes i >= 1 are drafted tokens.  Row (b, i)
+ * of the logits (fp32, at logits + (b N + i) ld) is the target's distribution
+ * of the token after node i, row (b, i) of draft_logits (nullable; ld_draft)
+ * the one its children were drawn from; NULL: the children are guesses without
+ * a distribution.  Both are taken at the given temperature, top-k and top-p,
+ * with the meaning of gpt2_sample except that exp is evaluated in 64 bits and
+ * ids are ordered by logit: w_i = rint(2^36 exp((z_i - max z) / temperature))
+ * over the first V columns, 0 outside the cuts; NaN counts as -infinity;
+ * temperature 0 keeps the highest logit alone (the smaller id on ties).
+ * From cur = 0, with S = sum w of cur's row and X = sum x of its draft row, for
+ * the children c of cur in increasing order, t = tokens[b N + c]:
+ *   accept c (cur = c) if u_c x_t S / X < w_t   (no draft: u_c S < w_t),
+ *   else w <- max(0, w - rint(x S / X))          (no draft: w_t <- 0)
+ * where a step that would leave no weight is not taken; with no child
+ * accepted, next[b] is the first id whose running weight exceeds u_0 S (the
+ * last id of positive weight if none does).  u_i = uniform[b N + i] (fp32 in
+ * [0, 1), clamped; every node its own number, the root's serves the draw).
+ * Drawn that way, the accepted tokens and next[b] have the target's
+ * distribution when the children of a node are drawn independently from its
+ * draft row, or are distinct guesses.
+ * path[b N + r] = the accepted nodes in order, node 0 first, -1 behind them;
+ * n_path[b] their number (>= 1); counts[b] = 0 gives n_path 0 and next -1.
+ * A token outside [0, V) is never accepted.  A node with parent -1 other than
+ * the root is never reached.  All integers exact and deterministic.
+ * GPT2_ERR_ARG unless 1 <= V <= 98304, V <= ld (and ld_draft), temperature >= 0
+ * and finite, top_k >= 0, 0 < top_p <= 1, 1 <= N <= 256. */
+int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits, int64_t ld_draft,
+                     const int32_t* tokens, const int32_t* parent, const int32_t* counts,
+                     const float* uniform, int B, int N, int V, float temperature, int top_k,
+                     float top_p, int32_t* path, int32_t* n_path, int32_t* next, void* stream);
+
+/* The keys and values of accepted nodes stored into the caches of n_layer
+ * layers [CS336: text generation]: for every layer l and r < n_path[b], cache
+ * row lens[b] + r of k_cache, v_cache (l-th block of [n_layer, B, Hkv, Tc, D])
+ * becomes the k, v part of row path[b N + r] of qkv ([n_layer, B, N] rows,
+ * ld_qkv apart).  path NULL: rows 0, 1, ...; n_path NULL: N each.
+ * new_lens[b] (nullable, not lens itself) = lens[b] + n_path[b].  Nothing else
+ * of the caches is touched.  A sequence whose rows would not fit (lens[b] < 0,
+ * n_path[b] outside 0 .. N, or lens[b] + n_path[b] > Tc) is left as it is, its
+ * new_lens[b] = lens[b]; a node index outside [0, N) is skipped; both are
+ * recorded for gpt2_device_error (GPT2_ERR_ARG). */
+int gpt2_kv_append(const void* qkv, int64_t ld_qkv, const int32_t* lens, const int32_t* path,
+                   const int32_t* n_path, int dtype, int n_layer, int B, int N, int H, int Hkv,
+                   int D, int Tc, void* k_cache, void* v_cache, int32_t* new_lens, void* stream);
+
 /* Self-check of the bounded device waits (no counterpart on the pages: the
  * failure handling of this library).  Every wait of the tensor-core kernels on
  * a barrier gives up after 2 s of device time, records a timeout (read back
@@ -535,9 +630,10 @@ int gpt2_wait_selfcheck(int* expired);
  * them per handle). */
 int gpt2_launch_count(int64_t* n);
 
-/* Reads and clears the device error word shared by the op-level calls
- * (bounded-wait timeouts).  *code = GPT2_OK when nothing was recorded.
- * Synchronises the device. */
+/* Reads and clears the device error word shared by the op-level calls:
+ * *code = GPT2_OK when nothing was recorded, GPT2_ERR_TIMEOUT for a bounded
+ * wait that gave up, GPT2_ERR_ARG for device-side contents out of range (the
+ * calls on drafted tokens); the last record wins.  Synchronises the device. */
 int gpt2_device_error(int* code);
 
 #ifdef __cplusplus

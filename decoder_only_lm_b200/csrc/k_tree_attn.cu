@@ -1,5 +1,5 @@
-// Attention of drafted tokens over a key/value cache, CUDA-core kernel: fp32
-// and bf16, head sizes 16, 32, 64 and 128.
+// Attention of drafted tokens over a key/value cache, the fp32 mode's
+// CUDA-core kernel, head sizes 16, 32, 64 and 128.
 //
 // Source: [ZERO] "GPT training", Attention (softmax(q k^T / sqrt(D)) v over the
 // positions a query may see); [CS336] section 5 (the cache that reuses the
@@ -25,13 +25,6 @@ __device__ __forceinline__ float4 load4(const T* p);
 template <>
 __device__ __forceinline__ float4 load4<float>(const float* p) {
   return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<bf16>(const bf16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 template <int D>
@@ -264,10 +257,14 @@ int launch_simt_d(const TreeAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+size_t tree_attn_mma_workspace(int N, int H, int Hkv, int D);
+int launch_tree_attn_mma(const TreeAttnArgs& a, cudaStream_t st);
+
 size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16_in) {
-  return size_t(2) * simt_grid() * slot_floats<MR>(D) * sizeof(float);
+  return bf16_in ? tree_attn_mma_workspace(N, H, Hkv, D)
+                 : size_t(2) * simt_grid() * slot_floats<MR>(D) * sizeof(float);
 }
 
 int launch_tree_attn(const TreeAttnArgs& a, int bf16_in, cudaStream_t st) {
-  return bf16_in ? launch_simt_d<bf16>(a, st) : launch_simt_d<float>(a, st);
+  return bf16_in ? launch_tree_attn_mma(a, st) : launch_simt_d<float>(a, st);
 }

@@ -16,6 +16,8 @@
 #pragma once
 
 #include "kernels.h"
+#include <type_traits>
+
 #include "tree_internal.h"
 
 namespace tree {

@@ -10,6 +10,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -604,40 +605,59 @@ def sample(logits, vocab, temperature=0.8, top_k=0, top_p=0.9, uniform=None, out
 
 
 # ------------------------------------------------------- decoding with drafted tokens
+# These calls are short enough on the device for the host's part to show, so
+# their common path avoids what costs microseconds: context managers, stream
+# objects, repeated size queries.
+def _elsewhere(t, stream):
+    """Whether a call on t's device needs another current device or stream."""
+    import torch
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
 def _on_device_of(t, stream):
     """Context in which a call on the tensors of t's device runs: that device
     current, and the caller's stream current (None: the device's current one),
     so that outputs and workspaces are allocated on the stream that uses them."""
-    import contextlib
-
     import torch
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
 
 
-def _arg(name, t, dtype, shape, device, optional=False):
-    """Checks one dense tensor argument."""
-    if t is None and optional:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or \
-            not t.is_contiguous():
+def _raw_stream(t):
+    """Handle of the current stream of t's device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _arg(name, t, dtype, shape, device):
+    """Checks one dense tensor argument; its address (None stays NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: needs a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _required(name, t):
+    if t is None:
+        raise ValueError(f"{name}: a tensor is needed")
+    return t
 
 
 def _node_rows(name, qkv, dims, H, Hkv, D):
     """Row stride of activations [..., N, (H + 2 Hkv) D] whose rows are evenly
     spaced over all leading dimensions."""
-    if qkv.dim() != dims or not qkv.is_cuda or qkv.shape[-1] != (H + 2 * Hkv) * D:
+    if qkv.dim() != dims or not qkv.is_cuda or H < 1 or qkv.shape[-1] != (H + 2 * Hkv) * D:
         raise ValueError(f"{name}: needs a cuda tensor of {dims} dimensions, the last one "
                          f"(n_head + 2 n_kv_head) * head size = {(H + 2 * Hkv) * D}, got "
                          f"{tuple(qkv.shape)} on {qkv.device}")
     ld = qkv.shape[-1]
+    if qkv.is_contiguous():
+        return ld
     for d in range(dims - 2, -1, -1):  # the spacing given by the innermost dimension that has one
         if qkv.shape[d] > 1:
             rows = 1
@@ -656,9 +676,20 @@ def _node_rows(name, qkv, dims, H, Hkv, D):
 
 
 def _act_type(name, t):
+    """gpt2 type code of activations."""
     import torch
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name}: float32 or bfloat16, got {t.dtype}")
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise ValueError(f"{name}: float32 or bfloat16, got {t.dtype}")
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_attention_bytes(B, N, H, Hkv, D, dt):
+    ws_b = C.c_size_t()
+    _check(lib.gpt2_tree_attention_workspace(B, N, H, Hkv, D, dt, C.byref(ws_b)))
+    return ws_b.value
 
 
 def tree_attention(qkv, k_cache, v_cache, lens, n_head, parent=None, counts=None, out=None,
@@ -674,36 +705,58 @@ def tree_attention(qkv, k_cache, v_cache, lens, n_head, parent=None, counts=None
     [B, n_head, N]); rows of nodes beyond counts are left as they were (0 in
     buffers allocated here)."""
     import torch
+    if not qkv.is_cuda:
+        raise ValueError(f"qkv: needs a cuda tensor, got one on {qkv.device}")
+    if _elsewhere(qkv, stream):
+        with _on_device_of(qkv, stream):
+            return tree_attention(qkv, k_cache, v_cache, lens, n_head, parent, counts, out, lse)
     if k_cache.dim() != 4:
         raise ValueError(f"k_cache: needs [B, n_kv_head, Tc, D], got {tuple(k_cache.shape)}")
     B, Hkv, Tc, D = k_cache.shape
-    _act_type("qkv", qkv)
+    dt, dtype, dev = _act_type("qkv", qkv), qkv.dtype, qkv.device
     ld = _node_rows("qkv", qkv, 3, n_head, Hkv, D)
-    N, dev = qkv.shape[1], qkv.device
+    N = qkv.shape[1]
     if qkv.shape[0] != B:
         raise ValueError(f"qkv has {qkv.shape[0]} sequences, the cache {B}")
-    _arg("k_cache", k_cache, qkv.dtype, (B, Hkv, Tc, D), dev)
-    _arg("v_cache", v_cache, qkv.dtype, (B, Hkv, Tc, D), dev)
-    _arg("lens", lens, torch.int32, (B,), dev)
-    _arg("parent", parent, torch.int32, (B, N), dev, optional=True)
-    _arg("counts", counts, torch.int32, (B,), dev, optional=True)
-    _arg("out", out, qkv.dtype, (B, N, n_head * D), dev, optional=True)
-    _arg("lse", lse, torch.float32, (B, n_head, N), dev, optional=True)
-    dt = _dtype_code(qkv)
-    ws_b = C.c_size_t()
-    _check(lib.gpt2_tree_attention_workspace(B, N, n_head, Hkv, D, dt, C.byref(ws_b)))
-    with _on_device_of(qkv, stream):
-        new = torch.empty if counts is None else torch.zeros
-        if out is None:
-            out = new((B, N, n_head * D), dtype=qkv.dtype, device=dev)
-        if lse is None:
-            lse = new((B, n_head, N), dtype=torch.float32, device=dev)
-        ws = torch.empty(ws_b.value, dtype=torch.uint8, device=dev)
-        _check(lib.gpt2_tree_attention(_ptr(qkv), ld, _ptr(k_cache), _ptr(v_cache), _ptr(lens),
-                                       _ptr(parent), _ptr(counts), dt, B, N, n_head, Hkv, D, Tc,
-                                       _ptr(out), n_head * D, _ptr(lse), _ptr(ws), ws_b.value,
-                                       _stream_ptr(stream)))
+    i32, f32 = torch.int32, torch.float32
+    pk = _arg("k_cache", k_cache, dtype, (B, Hkv, Tc, D), dev)
+    pv = _arg("v_cache", _required("v_cache", v_cache), dtype, (B, Hkv, Tc, D), dev)
+    pl = _arg("lens", _required("lens", lens), i32, (B,), dev)
+    pp = _arg("parent", parent, i32, (B, N), dev)
+    pc = _arg("counts", counts, i32, (B,), dev)
+    nbytes = _tree_attention_bytes(B, N, n_head, Hkv, D, dt)
+    if out is None:
+        new = qkv.new_empty if counts is None else qkv.new_zeros
+        out = new((B, N, n_head * D))
+        po = out.data_ptr()
+    else:
+        po = _arg("out", out, dtype, (B, N, n_head * D), dev)
+    if lse is None:
+        new = qkv.new_empty if counts is None else qkv.new_zeros
+        lse = new((B, n_head, N), dtype=f32)
+        pe = lse.data_ptr()
+    else:
+        pe = _arg("lse", lse, f32, (B, n_head, N), dev)
+    ws = qkv.new_empty(nbytes, dtype=torch.uint8)
+    rc = lib.gpt2_tree_attention(qkv.data_ptr(), ld, pk, pv, pl, pp, pc, dt, B, N, n_head, Hkv, D,
+                                 Tc, po, n_head * D, pe, ws.data_ptr(), nbytes, _raw_stream(qkv))
+    if rc:
+        _check(rc)
     return out, lse
+
+
+def _logit_rows(name, t, B, N, vocab, dev):
+    """Row stride of fp32 logits [B, N, >= vocab] with evenly spaced rows."""
+    import torch
+    if t.dtype is not torch.float32 or t.dim() != 3 or t.shape[0] != B or t.shape[1] != N or \
+            t.device != dev or t.shape[2] < vocab:
+        raise ValueError(f"{name}: needs float32 [{B}, {N}, >= {vocab}] on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return t.shape[2]
+    if t.stride(2) != 1 or (B > 1 and N > 1 and t.stride(0) != N * t.stride(1)):
+        raise ValueError(f"{name}: rows must be dense and evenly spaced, got strides {t.stride()}")
+    return t.stride(1) if N > 1 else t.stride(0) if B > 1 else t.shape[2]
 
 
 def tree_verify(logits, vocab, tokens, uniform, temperature=0.8, top_k=0, top_p=0.9, parent=None,
@@ -717,33 +770,30 @@ def tree_verify(logits, vocab, tokens, uniform, temperature=0.8, top_k=0, top_p=
     [B, N], accepted nodes in order from node 0 and -1 behind them; n_path int32
     [B]; next int32 [B])."""
     import torch
-    if logits.dim() != 3 or logits.dtype != torch.float32 or not logits.is_cuda:
+    if logits.dim() != 3 or not logits.is_cuda:
         raise ValueError("logits: needs a float32 cuda tensor [B, N, >= vocab]")
+    if _elsewhere(logits, stream):
+        with _on_device_of(logits, stream):
+            return tree_verify(logits, vocab, tokens, uniform, temperature, top_k, top_p, parent,
+                               draft_logits, counts)
     B, N, _ = logits.shape
-    dev = logits.device
-
-    def rows(name, t):
-        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[:2] != (B, N) or t.device != dev or \
-                t.shape[2] < vocab or t.stride(2) != 1 or \
-                (B > 1 and N > 1 and t.stride(0) != N * t.stride(1)):
-            raise ValueError(f"{name}: needs float32 rows [B, N, >= vocab], evenly spaced, got "
-                             f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-        return t.stride(1) if N > 1 else t.stride(0) if B > 1 else t.shape[2]
-
-    ld = rows("logits", logits)
-    ld_draft = 0 if draft_logits is None else rows("draft_logits", draft_logits)
-    _arg("tokens", tokens, torch.int32, (B, N), dev)
-    _arg("uniform", uniform, torch.float32, (B, N), dev)
-    _arg("parent", parent, torch.int32, (B, N), dev, optional=True)
-    _arg("counts", counts, torch.int32, (B,), dev, optional=True)
-    with _on_device_of(logits, stream):
-        path = torch.empty((B, N), dtype=torch.int32, device=dev)
-        n_path = torch.empty(B, dtype=torch.int32, device=dev)
-        nxt = torch.empty(B, dtype=torch.int32, device=dev)
-        _check(lib.gpt2_tree_verify(_ptr(logits), ld, _ptr(draft_logits), ld_draft, _ptr(tokens),
-                                    _ptr(parent), _ptr(counts), _ptr(uniform), B, N, vocab,
-                                    temperature, top_k, top_p, _ptr(path), _ptr(n_path), _ptr(nxt),
-                                    _stream_ptr(stream)))
+    dev, i32 = logits.device, torch.int32
+    ld = _logit_rows("logits", logits, B, N, vocab, dev)
+    ldd, pd = 0, None
+    if draft_logits is not None:
+        ldd, pd = _logit_rows("draft_logits", draft_logits, B, N, vocab, dev), draft_logits.data_ptr()
+    pt = _arg("tokens", _required("tokens", tokens), i32, (B, N), dev)
+    pu = _arg("uniform", _required("uniform", uniform), torch.float32, (B, N), dev)
+    pp = _arg("parent", parent, i32, (B, N), dev)
+    pc = _arg("counts", counts, i32, (B,), dev)
+    path = tokens.new_empty((B, N))
+    n_path = tokens.new_empty(B)
+    nxt = tokens.new_empty(B)
+    rc = lib.gpt2_tree_verify(logits.data_ptr(), ld, pd, ldd, pt, pp, pc, pu, B, N, vocab,
+                              temperature, top_k, top_p, path.data_ptr(), n_path.data_ptr(),
+                              nxt.data_ptr(), _raw_stream(logits))
+    if rc:
+        _check(rc)
     return path, n_path, nxt
 
 
@@ -754,25 +804,30 @@ def kv_append(qkv, k_cache, v_cache, lens, path=None, n_path=None, stream=None):
     place), lens int32 [B]; path, n_path as tree_verify returns them (None: the
     nodes in order, all of them).  Returns the new lengths, int32 [B]."""
     import torch
+    if not qkv.is_cuda:
+        raise ValueError(f"qkv: needs a cuda tensor, got one on {qkv.device}")
+    if _elsewhere(qkv, stream):
+        with _on_device_of(qkv, stream):
+            return kv_append(qkv, k_cache, v_cache, lens, path, n_path)
     if k_cache.dim() != 5:
         raise ValueError(f"k_cache: needs [n_layer, B, n_kv_head, Tc, D], got {tuple(k_cache.shape)}")
     L, B, Hkv, Tc, D = k_cache.shape
-    _act_type("qkv", qkv)
+    dt, dtype, dev, i32 = _act_type("qkv", qkv), qkv.dtype, qkv.device, torch.int32
     H = qkv.shape[-1] // D - 2 * Hkv
     ld = _node_rows("qkv", qkv, 4, H, Hkv, D)
-    N, dev = qkv.shape[2], qkv.device
-    if qkv.shape[:2] != (L, B):
+    N = qkv.shape[2]
+    if qkv.shape[0] != L or qkv.shape[1] != B:
         raise ValueError(f"qkv has {tuple(qkv.shape[:2])} layers and sequences, the cache {(L, B)}")
-    _arg("k_cache", k_cache, qkv.dtype, (L, B, Hkv, Tc, D), dev)
-    _arg("v_cache", v_cache, qkv.dtype, (L, B, Hkv, Tc, D), dev)
-    _arg("lens", lens, torch.int32, (B,), dev)
-    _arg("path", path, torch.int32, (B, N), dev, optional=True)
-    _arg("n_path", n_path, torch.int32, (B,), dev, optional=True)
-    with _on_device_of(qkv, stream):
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        _check(lib.gpt2_kv_append(_ptr(qkv), ld, _ptr(lens), _ptr(path), _ptr(n_path),
-                                  _dtype_code(qkv), L, B, N, H, Hkv, D, Tc, _ptr(k_cache),
-                                  _ptr(v_cache), _ptr(new_lens), _stream_ptr(stream)))
+    pk = _arg("k_cache", k_cache, dtype, (L, B, Hkv, Tc, D), dev)
+    pv = _arg("v_cache", _required("v_cache", v_cache), dtype, (L, B, Hkv, Tc, D), dev)
+    pl = _arg("lens", _required("lens", lens), i32, (B,), dev)
+    pp = _arg("path", path, i32, (B, N), dev)
+    pn = _arg("n_path", n_path, i32, (B,), dev)
+    new_lens = lens.new_empty(B)
+    rc = lib.gpt2_kv_append(qkv.data_ptr(), ld, pl, pp, pn, dt, L, B, N, H, Hkv, D, Tc, pk, pv,
+                            new_lens.data_ptr(), _raw_stream(qkv))
+    if rc:
+        _check(rc)
     return new_lens
 
 

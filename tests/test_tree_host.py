@@ -101,7 +101,7 @@ def test_row_spacing_of_views(g):
         is_cuda, device = True, "cuda:0"
 
         def __init__(self, t):
-            self.shape, self.s = t.shape, t.stride()
+            self.shape, self.s, self.is_contiguous = t.shape, t.stride(), t.is_contiguous
 
         def dim(self):
             return len(self.shape)

@@ -2,7 +2,6 @@
 // cache store.  Argument checks on the host; the kernels check what lives on
 // the device (lengths, counts, trees, paths).
 
-#include <cmath>
 #include <string>
 
 #include "kernels.h"
@@ -78,8 +77,8 @@ int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits,
     return refuse("tree_verify: null pointer");
   if (B < 1 || B > 65535 || N < 1 || N > kTreeMaxNodes || V < 1 || V > kTreeMaxVocab || ld < V ||
       (draft_logits && ld_draft < V))
-    return refuse("tree_verify: B, N (1..256), V (1..98304) or a row stride out of range");
-  if (!(temperature >= 0.f) || !std::isfinite(temperature) || top_k < 0 ||
+    return refuse("tree_verify: B, N (1..256), V (1..65536) or a row stride out of range");
+  if (!(temperature >= 0.f && temperature <= 1e30f) || top_k < 0 ||
       !(top_p > 0.f && top_p <= 1.f))
     return refuse("tree_verify: bad sampling settings");
   try {

@@ -19,12 +19,16 @@
 // (kept as they were if nothing would be left); after the last child the next
 // token is the first id whose running weight exceeds u_0 S.
 //
-// One cluster of up to 8 CTAs per sequence, each with a slice of the vocabulary
-// in shared memory; only the rows of nodes that the walk reaches are read (a
-// tree of 64 with 3 accepted tokens: 4 of 64 rows).  A node costs one exchange
-// over the cluster for the maximum, one for the sum, one for each rejected
-// child; the children's own weights are fetched once and kept up to date by
-// every CTA.  What bounds it is the latency of that chain, not bandwidth.
+// One cluster of 8 CTAs per sequence, each with a slice of the vocabulary; only
+// the rows of nodes that the walk reaches are read (a tree of 64 with 3 accepted
+// tokens: 4 of 64 rows).  What bounds it is the latency of that chain, so a node
+// costs as few exchanges over the cluster as it can: one for the maxima of both
+// rows, one for their sums or two for their cuts (which give the sums too), and
+// one for each rejected child of a drafted row.  Every exchange pushes a CTA's
+// values into the others' shared memory before the cluster barrier, so that
+// behind it all reads are local; the work between two barriers that does not
+// grow with the vocabulary is left to one warp.  A child's own weights need no
+// exchange: every CTA computes them from the logits.
 
 #include <cooperative_groups.h>
 
@@ -37,33 +41,53 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;
-constexpr int kCand = 64;  // candidates of a cut per CTA before the bisection takes over
+constexpr int kCluster = 8;
+constexpr int kMaxSlice = kTreeMaxVocab / kCluster;
+constexpr int kPer = kMaxSlice / kThreads;  // ids of a thread at most
+constexpr int kIlp = 8;                     // weights of a thread computed together
+constexpr int kCoarse = 37;          // bins by the exponent of a weight (1 .. 2^36)
+constexpr int kBins = kCoarse * 32;  // ... and the 5 bits behind its leading one
+constexpr int kCand = 48;            // ids of a cut's bin per CTA; more are bisected
 constexpr double kOne = 68719476736.0;  // 2^36
+constexpr unsigned kAll = 0xffffffffu;
+
+// A row's cuts.  hist: this CTA's weights (in halves of 18 bits; a slice holds at
+// most 2^13 ids, so 32 bits hold every sum) and ids by bin.
+struct Cut {
+  uint32_t lo[kBins], hi[kBins], count[kBins];
+  // pushed by every CTA: weights and ids by coarse bin
+  uint64_t in_w[kCluster][kCoarse];
+  uint32_t in_n[kCluster][kCoarse];
+  // the fine bins of the coarse bin that a cut falls into, of every CTA
+  uint64_t fine_w[kCluster][32];
+  uint32_t fine_n[kCluster][32];
+  // pushed by every CTA: the ids of the cut's bin, for the top-k and top-p cut
+  uint64_t key[2][kCluster][kCand], w[2][kCluster][kCand];
+  uint32_t n_in[2][kCluster];
+  uint32_t n_mine[2];
+  int coarse, bin;  // where the cut falls, -1: nowhere
+  uint64_t at_n, at_w;  // ids and weight of the bins above it
+  double goal;
+  uint64_t tau, kept;  // lowest ordering key that stays, weight that stays
+};
 
 struct Shared {
-  uint64_t warp_red[2][3][kWarps];
-  uint64_t red[2][3];
-  uint32_t hist_lo[2][kBins], hist_hi[2][kBins];
-  uint64_t tot[kBins];
-  uint64_t cand_key[kCand], cand_w[kCand];
-  uint64_t all_key[kCand * kMaxCluster], all_w[kCand * kMaxCluster];
-  uint32_t n_cand;
-  int bin, found;
-  uint64_t before;
-  uint64_t tau;
+  uint64_t warp_red[2][2][kWarps];
+  uint64_t red[2][2][kCluster];  // pushed
   int tok[kTreeMaxNodes], par[kTreeMaxNodes], kid[kTreeMaxNodes];
+  float u[kTreeMaxNodes];
   uint64_t kw[kTreeMaxNodes], kx[kTreeMaxNodes];
+  double exp_table[64];
   int n_kids;
-  int pick;
 };
 
 // Order of the ids of a row: by logit, the smaller id first among equal ones.
-__device__ __forceinline__ uint64_t order_key(float z, int id) {
+__device__ __forceinline__ uint32_t order_of(float z) {
   const uint32_t b = __float_as_uint(z + 0.f);  // -0 counts as 0
-  const uint32_t ord = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return (uint64_t(ord) << 32) | uint64_t(0xFFFFFFFFu - uint32_t(id));
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(float z, int id) {
+  return (uint64_t(order_of(z)) << 32) | uint64_t(0xFFFFFFFFu - uint32_t(id));
 }
 __device__ __forceinline__ float key_logit(uint64_t key) {
   const uint32_t ord = uint32_t(key >> 32);
@@ -71,254 +95,342 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
 }
 __device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z; }
 
-struct Max {
-  __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
+// rint(2^36 exp(-d / T)) for d = zmax - z >= 0 (zmax finite).  With x = 64 d
+// log2(e) / T = r - n, n the nearest integer (from the 1.5 * 2^52 shift):
+// 2^36 exp(-d / T) = 2^(36 + n / 64) 2^(r / 64), the first factor from a table of
+// 64 and an exponent, the second from its Taylor sum, |r ln2 / 64| < 0.0055: the
+// first term left out is below 4e-17.  A weight is within 2^-14 of the value it
+// rounds.  Returned as 2^52 + weight, whose low 52 bits are the integer.
+constexpr double kOnes = 4503599627370496.0;  // 2^52
+struct Exp {
+  const double* table;  // 2^(36 + i / 64)
+  double per_unit;      // -64 log2(e) / T
+  // logits below it have weight 0: 2^36 exp(-40) < 1/2 (NaN and -inf with them)
+  __device__ static float floor_of(float zmax, float T) { return fmaxf(zmax - 40.f * T, -3e38f); }
+  __device__ double operator()(float z, float zmax, float zmin) const {
+    constexpr double kShift = 6755399441055744.0;  // 1.5 * 2^52
+    constexpr double c = 0.010830424696249145;     // ln(2) / 64
+    const double d = double(zmax) - double(fmaxf(z, zmin));
+    const double t = fma(d, per_unit, kShift);
+    const double r = fma(d, per_unit, kShift - t);
+    const int n = __double2loint(t);
+    double p = fma(r, c * c * c * c * c / 120, c * c * c * c / 24);
+    p = fma(r, p, c * c * c / 6);
+    p = fma(r, p, c * c / 2);
+    p = fma(r, p, c);
+    p = fma(r, p, 1.0) * table[n & 63];
+    return __hiloint2double(__double2hiint(p) + ((n & ~63) << 14), __double2loint(p)) + kOnes;
+  }
 };
-struct Add {
-  __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a + b; }
+__device__ __forceinline__ uint64_t integer_of(double v) {
+  return uint64_t(__double_as_longlong(v)) & 0xFFFFFFFFFFFFFull;
+}
+
+// Bin of a weight >= 1 (as 2^52 + weight): its exponent and the 5 bits behind
+// the leading one; the bin's weights are [bin_low(bin), bin_low(bin + 1)).
+__device__ __forceinline__ int bin_of(double v) {
+  return (__double2hiint(v - kOnes) >> 15) - (1023 << 5);
+}
+__device__ __forceinline__ uint64_t bin_low(int bin) {
+  const uint64_t m = uint64_t(32 + (bin & 31)) << (bin >> 5);
+  return (m + 31) >> 5;  // small exponents have fewer than 32 weights
+}
+
+// Sum over a warp of values below 2^53: three parts of 21 bits, 32 of which fit
+// 32 bits.
+__device__ __forceinline__ uint64_t warp_add(uint64_t v) {
+  const uint64_t a = __reduce_add_sync(kAll, uint32_t(v) & 0x1FFFFFu);
+  const uint64_t b = __reduce_add_sync(kAll, uint32_t(v >> 21) & 0x1FFFFFu);
+  const uint64_t c = __reduce_add_sync(kAll, uint32_t(v >> 42));
+  return a + (b << 21) + (c << 42);
+}
+__device__ __forceinline__ uint64_t warp_top(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(kAll, uint32_t(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
+  return (uint64_t(hi) << 32) | lo;
+}
+// Inclusive running sum over a warp's lanes.
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kAll, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+struct Row {
+  const float* z;  // logits
+  uint64_t* w;     // weights of this CTA's ids
+  Cut* cut;
+  uint64_t top;    // ordering key of the maximum
+  uint64_t sum;    // of all weights
+  uint64_t tau;    // lowest ordering key that stays
+  uint64_t low;    // weights below this went with the cuts, those of the cut's
+  uint64_t high;   // bin, [low, high), by their ordering keys
 };
 
 struct Walk {
   Shared& sh;
   cg::cluster_group cl;
-  int lane, warp, rank, cs;
-  int lo, n;  // this CTA's ids [lo, lo + n)
-  int turn;   // exchange buffer of the next reduction
+  int lane, warp, rank;
+  int lo, n;   // this CTA's ids [lo, lo + n)
+  int i0, i1;  // this warp's part of them, lane by lane
+  int turn;    // exchange buffer of the next reduction
 
-  // Block-wide reductions of K values exchanged over the cluster: afterwards
-  // lane c < cs of every warp holds CTA c's values (0 elsewhere).  Two buffers
-  // in turn: the barrier of the next exchange orders this one's reads before
-  // the buffer is written again.
-  template <int K, typename Op>
-  __device__ void exchange(uint64_t (&v)[K], Op op) {
+  template <typename T>
+  __device__ T* remote(T* p, int r) {
+    return cl.map_shared_rank(p, r);
+  }
+
+  // K sums (or maxima) over the cluster.  Two buffers in turn: a CTA pushes into
+  // one again only behind the next exchange's barrier, which the others reach
+  // after reading it.
+  template <int K, bool kMax>
+  __device__ void exchange(uint64_t (&v)[K]) {
     const int t = turn;
     turn ^= 1;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], o));
-      if (lane == 0) sh.warp_red[t][k][warp] = v[k];
+      const uint64_t x = kMax ? warp_top(v[k]) : warp_add(v[k]);
+      if (lane == 0) sh.warp_red[t][k][warp] = x;
     }
     __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        uint64_t x = sh.warp_red[t][k][lane & (kWarps - 1)];
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-        if (lane == 0) sh.red[t][k] = x;
-      }
+    if (warp < K) {
+      const uint64_t mine = lane < kWarps ? sh.warp_red[t][warp][lane] : 0;
+      const uint64_t x = kMax ? warp_top(mine) : warp_add(mine);
+      if (lane < kCluster) *remote(&sh.red[t][warp][rank], lane) = x;
     }
     cl.sync();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      v[k] = 0;
-      if (lane < cs) v[k] = *cl.map_shared_rank(&sh.red[t][k], lane);
+      v[k] = sh.red[t][k][0];
+#pragma unroll
+      for (int r = 1; r < kCluster; ++r) {
+        const uint64_t x = sh.red[t][k][r];
+        v[k] = kMax ? (x > v[k] ? x : v[k]) : v[k] + x;
+      }
     }
   }
-  // over the (at most 8) lanes that hold the CTAs' values
-  template <typename Op>
-  __device__ uint64_t over(uint64_t v, Op op) {
+
+  // One warp: the coarse bin at which the ids counted from the top (by_weight
+  // false) or their weight reach the goal, with what lies above it.
+  __device__ void find_coarse(Cut& c, bool by_weight, double share) {
+    // lane l: coarse bins 36 - 2 l and 35 - 2 l, from the top
+    uint64_t un[2] = {0, 0}, uw[2] = {0, 0};
 #pragma unroll
-    for (int o = kMaxCluster / 2; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return __shfl_sync(0xffffffffu, v, 0);
+    for (int j = 0; j < 2; ++j) {
+      const int k = kCoarse - 1 - 2 * lane - j;
+      if (k >= 0)
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) {
+          un[j] += c.in_n[r][k];
+          uw[j] += c.in_w[r][k];
+        }
+    }
+    const uint64_t in = warp_scan(un[0] + un[1], lane), iw = warp_scan(uw[0] + uw[1], lane);
+    const uint64_t total = __shfl_sync(kAll, iw, 31);
+    // share: of the whole weight (no top-k cut before); else the goal stands
+    const double goal = share > 0.0 ? share * double(total) : c.goal;
+    const unsigned hit = __ballot_sync(kAll, double(by_weight ? iw : in) >= goal);
+    if (!hit) {  // fewer ids of positive weight than the goal: all stay
+      if (lane == 0) {
+        c.coarse = c.bin = -1;
+        c.kept = total;
+      }
+      return;
+    }
+    if (lane == __ffs(int(hit)) - 1) {
+      uint64_t an = in - un[0] - un[1], aw = iw - uw[0] - uw[1];
+      int k = kCoarse - 1 - 2 * lane;
+      if (double(by_weight ? aw + uw[0] : an + un[0]) < goal) {
+        an += un[0];
+        aw += uw[0];
+        --k;
+      }
+      c.coarse = k;
+      c.at_n = an;
+      c.at_w = aw;
+      c.goal = goal;
+    }
+  }
+  // One warp: the bin within it (lane 0 the topmost).
+  __device__ void find_fine(Cut& c, bool by_weight) {
+    uint64_t fn = 0, fw = 0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      fn += c.fine_n[r][lane];
+      fw += c.fine_w[r][lane];
+    }
+    const uint64_t an = c.at_n, aw = c.at_w;
+    const uint64_t in = an + warp_scan(fn, lane), iw = aw + warp_scan(fw, lane);
+    const unsigned hit = __ballot_sync(kAll, double(by_weight ? iw : in) >= c.goal);
+    if (lane == __ffs(int(hit)) - 1) {
+      c.bin = c.coarse * 32 + 31 - lane;
+      c.at_n = in - fn;
+      c.at_w = c.kept = iw - fw;
+    }
   }
 
-  // Distance of a logit below the row's maximum.
-  static __device__ double below(float zmax, float z) {
-    return z == zmax ? 0.0 : double(zmax) - double(z);
-  }
-
-  // Keeps the ids before the first at which the running count (by_weight
-  // false, goal = k) or weight (goal = a weight) of the ordered ids has reached
-  // the goal, that one included; the others' weights become 0.  Ids of weight
-  // 0 do not matter either way.  Two levels of a 256-bin histogram over the
-  // distance below the maximum narrow the place down to a few ids, which
-  // every CTA then orders exactly; if there are many (equal logits), it bisects
-  // over the ordering keys.
-  __device__ void cut(const float* z, uint64_t* w, float zmax, double T, bool by_weight,
-                      double goal) {
-    const double scale = kBins / (26.0 * T);
-    int bin[2];
-    uint64_t before = 0;
-    bool none = false;
-    for (int level = 0; level < 2 && !none; ++level) {
-      for (int i = threadIdx.x; i < kBins; i += kThreads)
-        sh.hist_lo[level][i] = sh.hist_hi[level][i] = 0;
-      if (threadIdx.x == 0) sh.found = -1;
-      __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint64_t wi = w[i];
-        if (wi == 0) continue;
-        const double d = below(zmax, clean(z[lo + i])) * scale;
-        int at = min(kBins - 1, int(d));
-        if (level == 1) {
-          if (at != bin[0]) continue;
-          at = max(0, min(kBins - 1, int((d - bin[0]) * kBins)));
-        }
-        if (by_weight) {
-          // sums of 18-bit halves over a slice of at most 2^14 ids fit 32 bits
-          atomicAdd(&sh.hist_lo[level][at], uint32_t(wi & 0x3FFFF));
-          atomicAdd(&sh.hist_hi[level][at], uint32_t(wi >> 18));
-        } else {
-          atomicAdd(&sh.hist_lo[level][at], 1u);
+  // A cut of the rows: the ids before the first at which the running count
+  // (by_weight false: to c.goal ids) or weight reaches the goal stay, that one
+  // included.  The bin of the place comes from the histograms; its ids are
+  // pushed to every CTA, which orders them.  Sets tau, sum, low and high.
+  template <int K>
+  __device__ void settle(Row (&row)[K], int rows, bool by_weight, double share) {
+    const int phase = by_weight;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < rows && warp == k) find_coarse(*row[k].cut, by_weight, share);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)  // warps 8 k .. 8 k + 7: one CTA's fine bins each
+      if (k < rows && warp / kCluster == k && row[k].cut->coarse >= 0) {
+        Cut& c = *row[k].cut;
+        const int r = warp % kCluster, f = c.coarse * 32 + 31 - lane;
+        const uint32_t a = *remote(&c.lo[f], r), h = *remote(&c.hi[f], r);
+        const uint32_t m = *remote(&c.count[f], r);
+        c.fine_w[r][lane] = a + (uint64_t(h) << 18);
+        c.fine_n[r][lane] = m;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < rows && warp == k && row[k].cut->coarse >= 0) {
+        Cut& c = *row[k].cut;
+        find_fine(c, by_weight);
+        if (lane == 0) {
+          c.tau = ~uint64_t(0);
+          c.n_mine[phase] = 0;
         }
       }
-      cl.sync();
-      if (threadIdx.x < kBins) {
-        uint64_t t = 0;
-        for (int c = 0; c < cs; ++c) {
-          t += *cl.map_shared_rank(&sh.hist_lo[level][threadIdx.x], c);
-          t += uint64_t(*cl.map_shared_rank(&sh.hist_hi[level][threadIdx.x], c)) << 18;
-        }
-        sh.tot[threadIdx.x] = t;
-      }
-      __syncthreads();
-      if (warp == 0) {  // lane l scans bins [8 l, 8 l + 8)
-        uint64_t mine[8], s = 0;
+    __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mine[j] = sh.tot[lane * 8 + j];
-          s += mine[j];
-        }
-        uint64_t incl = s;
+    for (int k = 0; k < K; ++k)
+      if (k < rows && row[k].cut->coarse >= 0) {
+        Cut& c = *row[k].cut;
+        row[k].low = bin_low(c.bin);
+        row[k].high = bin_low(c.bin + 1);
+#pragma unroll 4
+        for (int i = i0 + lane; i < i1; i += 32) {
+          const uint64_t w = row[k].w[i];
+          if (w < row[k].low || w >= row[k].high) continue;
+          const uint64_t key = order_key(clean(row[k].z[lo + i]), lo + i);
+          if (key < row[k].tau) continue;  // cut away already
+          const uint32_t at = atomicAdd(&c.n_mine[phase], 1u);
+          if (at < kCand)
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        uint64_t at = before + incl - s;
-        const bool here = double(before + incl) >= goal && double(at) < goal;
-        if (here) {
-          for (int j = 0; j < 8; ++j) {
-            if (double(at + mine[j]) >= goal) {
-              sh.found = lane * 8 + j;
-              sh.before = at;
-              break;
+            for (int r = 0; r < kCluster; ++r) {
+              *remote(&c.key[phase][rank][at], r) = key;
+              *remote(&c.w[phase][rank][at], r) = w;
             }
-            at += mine[j];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < rows && threadIdx.x < kCluster)
+        *remote(&row[k].cut->n_in[phase][rank], threadIdx.x) = row[k].cut->n_mine[phase];
+    cl.sync();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < rows && row[k].cut->coarse >= 0) {
+        Cut& c = *row[k].cut;
+        uint32_t most = 0;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) most = max(most, c.n_in[phase][r]);
+        if (most > kCand) {  // the same choice in every CTA
+          bisect(row[k], c, by_weight);
+          continue;
+        }
+        // one warp per id, its lanes over the others
+        const uint64_t above = by_weight ? c.at_w : c.at_n;
+        const int grid = kCluster * int(most);
+        for (int e = warp; e < grid; e += kWarps) {
+          const int r0 = e % kCluster, j0 = e / kCluster;
+          if (j0 >= int(c.n_in[phase][r0])) continue;
+          const uint64_t key = c.key[phase][r0][j0];
+          uint64_t ahead = 0;
+          for (int q = lane; q < grid; q += 32) {
+            const int r = q % kCluster, j = q / kCluster;
+            if (j < int(c.n_in[phase][r]) && c.key[phase][r][j] > key)
+              ahead += by_weight ? c.w[phase][r][j] : 1;
+          }
+          ahead = warp_add(ahead);
+          if (lane == 0 && double(above + ahead) < c.goal) {
+            atomicMin(reinterpret_cast<unsigned long long*>(&c.tau), (unsigned long long)key);
+            atomicAdd(reinterpret_cast<unsigned long long*>(&c.kept),
+                      (unsigned long long)c.w[phase][r0][j0]);
           }
         }
       }
-      __syncthreads();
-      bin[level] = sh.found;
-      if (bin[level] < 0)
-        none = true;  // everything is kept
-      else
-        before = sh.before;
-      __syncthreads();
-    }
-    if (none) {  // the same in every CTA
-      cl.sync();   // the histograms are read no more
-      return;
-    }
-    // the ids of the bin
-    if (threadIdx.x == 0) {
-      sh.n_cand = 0;
-      sh.tau = ~uint64_t(0);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k < rows) {
+        row[k].sum = row[k].cut->kept;
+        if (row[k].cut->coarse >= 0) row[k].tau = row[k].cut->tau;
+      }
+  }
+  // The same for a bin with many ids (equal logits): the largest key t such
+  // that the ids of key >= t reach the goal, bit by bit.
+  __device__ void bisect(const Row& row, Cut& c, bool by_weight) {
+    const uint64_t above = by_weight ? c.at_w : c.at_n;
+    uint64_t tau = 0, kept = 0;
+    for (int bit = 63; bit >= -1; --bit) {  // the last round: the weight of what stays
+      const uint64_t t = bit >= 0 ? tau | (uint64_t(1) << bit) : tau;
+      uint64_t v[2] = {0, 0};
+      for (int i = i0 + lane; i < i1; i += 32) {
+        const uint64_t w = row.w[i];
+        if (w < row.low || w >= row.high) continue;
+        const uint64_t key = order_key(clean(row.z[lo + i]), lo + i);
+        if (key < row.tau || key < t) continue;
+        v[0] += by_weight ? w : 1;
+        v[1] += w;
+      }
+      exchange<2, false>(v);
+      kept = v[1];
+      if (bit >= 0 && double(above + v[0]) >= c.goal) tau = t;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      if (w[i] == 0) continue;
-      const float zi = clean(z[lo + i]);
-      const double d = below(zmax, zi) * scale;
-      if (min(kBins - 1, int(d)) != bin[0]) continue;
-      if (max(0, min(kBins - 1, int((d - bin[0]) * kBins))) != bin[1]) continue;
-      const uint32_t at = atomicAdd(&sh.n_cand, 1u);
-      if (at < kCand) {
-        sh.cand_key[at] = order_key(zi, lo + i);
-        sh.cand_w[at] = w[i];
-      }
+    if (threadIdx.x == 0) {
+      c.tau = tau;
+      c.kept = c.at_w + kept;
     }
-    cl.sync();
-    uint32_t cnt = 0;
-    if (lane < cs) cnt = *cl.map_shared_rank(&sh.n_cand, lane);
-    const bool many = __any_sync(0xffffffffu, cnt > kCand);
-    uint64_t tau;
-    if (!many) {
-      uint32_t incl = cnt;  // where each CTA's candidates go in the joint list
-#pragma unroll
-      for (int o = 1; o < kMaxCluster; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const int total = int(__shfl_sync(0xffffffffu, incl, kMaxCluster - 1));
-      for (int c = warp; c < cs; c += kWarps) {
-        const int nc = int(__shfl_sync(0xffffffffu, cnt, c));
-        const int off = int(__shfl_sync(0xffffffffu, incl, c)) - nc;
-        for (int j = lane; j < nc; j += 32) {
-          sh.all_key[off + j] = *cl.map_shared_rank(&sh.cand_key[j], c);
-          sh.all_w[off + j] = *cl.map_shared_rank(&sh.cand_w[j], c);
-        }
-      }
-      __syncthreads();
-      for (int j = threadIdx.x; j < total; j += kThreads) {
-        const uint64_t key = sh.all_key[j];
-        uint64_t excl = before;
-        for (int i = 0; i < total; ++i)
-          if (sh.all_key[i] > key) excl += by_weight ? sh.all_w[i] : 1;
-        if (double(excl) < goal)
-          atomicMin(reinterpret_cast<unsigned long long*>(&sh.tau), (unsigned long long)key);
-      }
-      __syncthreads();
-      tau = sh.tau;
-    } else {
-      // largest t whose ids of key >= t reach the goal
-      uint64_t a = 0;
-      for (int bit = 63; bit >= 0; --bit) {
-        const uint64_t t = a | (uint64_t(1) << bit);
-        uint64_t v[1] = {0};
-        for (int i = threadIdx.x; i < n; i += kThreads)
-          if (w[i] && order_key(clean(z[lo + i]), lo + i) >= t) v[0] += by_weight ? w[i] : 1;
-        exchange(v, Add());
-        if (double(over(v[0], Add())) >= goal) a = t;
-      }
-      tau = a;
-    }
-    for (int i = threadIdx.x; i < n; i += kThreads)
-      if (w[i] && order_key(clean(z[lo + i]), lo + i) < tau) w[i] = 0;
+    __syncthreads();
   }
 
-  // Weights of a row from its logits (top: the ordering key of its maximum).
-  __device__ void weights(const float* z, uint64_t* w, uint64_t top, double T, int top_k,
-                          double top_p) {
-    const float zmax = key_logit(top);
-    const int arg = int(0xFFFFFFFFu - uint32_t(top));
-    if (T == 0.0) {
-      for (int i = threadIdx.x; i < n; i += kThreads) w[i] = lo + i == arg ? uint64_t(kOne) : 0;
-      return;
-    }
-    const double far = 26.0 * T;  // 2^36 exp(-26) < 1/2
+  // Removes what the cuts removed from a row's weights (only the rows that are
+  // drawn from or subtracted need it).
+  __device__ void trim(const Row& row) {
+    if (row.tau == 0) return;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const double d = below(zmax, __uint_as_float(uint32_t(w[i])));
-      w[i] = d > far ? 0 : uint64_t(__double2ll_rn(exp(-d / T) * kOne));
-    }
-    if (top_k > 0) cut(z, w, zmax, T, false, double(top_k));
-    if (top_p < 1.0) {
-      uint64_t v[1] = {0};
-      for (int i = threadIdx.x; i < n; i += kThreads) v[0] += w[i];
-      exchange(v, Add());
-      cut(z, w, zmax, T, true, top_p * double(over(v[0], Add())));
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const uint64_t w = row.w[i];
+      if (w < row.low || (w < row.high && order_key(clean(row.z[lo + i]), lo + i) < row.tau))
+        row.w[i] = 0;
     }
   }
 };
 
+template <bool kDraft, bool kCuts>
 __global__ void __launch_bounds__(kThreads) tree_verify_kernel(TreeVerifyArgs a, int slice) {
-  extern __shared__ uint64_t rows[];  // w[slice], then x[slice] when a draft is given
+  constexpr int K = kDraft ? 2 : 1;
+  extern __shared__ uint64_t dyn[];  // w[slice], x[slice] (draft), the rows' cuts
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x;
-  const int cs = int(cl.num_blocks()), rank = int(cl.block_rank());
-  const int b = blockIdx.x / cs;
-  Walk wk{sh, cl, tid & 31, tid >> 5, rank, cs, 0, 0, 0};
+  const int rank = int(cl.block_rank()), b = blockIdx.x / kCluster;
+  Walk wk{sh, cl, tid & 31, tid >> 5, rank, 0, 0, 0, 0, 0};
   const int lane = wk.lane;
   wk.lo = min(a.V, rank * slice);
   wk.n = min(a.V, wk.lo + slice) - wk.lo;
-  uint64_t* w = rows;
-  uint64_t* x = a.draft ? rows + slice : nullptr;
+  const int per = (slice + kThreads - 1) / kThreads;  // ids of a lane
+  wk.i0 = min(wk.n, wk.warp * per * 32);
+  wk.i1 = min(wk.n, wk.i0 + per * 32);
   const double T = double(a.temperature), top_p = double(a.top_p);
   const int top_k = a.top_k < a.V ? a.top_k : 0;
+  Cut* cut = reinterpret_cast<Cut*>(dyn + slice * K);
   const float* u = a.uniform + int64_t(b) * a.N;
   int32_t* path = a.path + int64_t(b) * a.N;
   auto unit = [](float v) { return double(fminf(fmaxf(v, 0.f), 1.f)); };
@@ -329,12 +441,14 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(TreeVerifyArgs a,
   for (int i = tid; i < a.N; i += kThreads) {
     if (rank == 0) path[i] = i == 0 && N > 0 ? 0 : -1;
     sh.tok[i] = a.tokens[int64_t(b) * a.N + i];
+    sh.u[i] = u[i];
     const int p = a.parent ? a.parent[int64_t(b) * a.N + i] : i - 1;
     if (i < N && (p < -1 || p >= i)) bad = true;
     sh.par[i] = p;
   }
   if (bad && rank == 0) atomicExch(a.err, kTreeBadInput);
-  __syncthreads();
+  if (tid < 64) sh.exp_table[tid] = exp2(36.0 + tid / 64.0);
+  const Exp ex{sh.exp_table, -64.0 * 1.4426950408889634 / T};
   if (N == 0) {  // the whole cluster
     if (rank == 0 && tid == 0) {
       a.n_path[b] = 0;
@@ -342,106 +456,226 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(TreeVerifyArgs a,
     }
     return;
   }
+  cl.sync();  // every CTA has started: the others may write into its shared memory
 
   int cur = 0, n_path = 1;
   while (true) {
+    // the rows' logits, all in flight; leaves need no draft row
+    const int64_t at = int64_t(b) * a.N + cur;
+    Row row[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      row[k].z = k ? a.draft + at * a.ld_draft : a.logits + at * a.ld;
+      row[k].w = dyn + slice * k;
+      row[k].cut = cut + k;
+      row[k].tau = row[k].low = row[k].high = 0;
+    }
+    float v[K][kPer];
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = wk.i0 + 32 * j + lane;
+        v[k][j] = j < per && i < wk.i1 ? __ldg(row[k].z + wk.lo + i) : -INFINITY;
+      }
+    };
+    fetch(0);
     // children of cur, in id order
     if (wk.warp == 0) {
-      int k = 0;
-      for (int i0 = cur + 1; i0 < N; i0 += 32) {
-        const int i = i0 + lane;
-        const bool is = i < N && sh.par[i] == cur;
-        const unsigned m = __ballot_sync(0xffffffffu, is);
-        if (is) sh.kid[k + __popc(m & ((1u << lane) - 1))] = i;
-        k += __popc(m);
+      int m = 0;
+      for (int j0 = cur + 1; j0 < N; j0 += 32) {
+        const int j = j0 + lane;
+        const bool is = j < N && sh.par[j] == cur;
+        const unsigned which = __ballot_sync(kAll, is);
+        if (is) sh.kid[m + __popc(which & ((1u << lane) - 1))] = j;
+        m += __popc(which);
       }
-      if (lane == 0) sh.n_kids = k;
+      if (lane == 0) sh.n_kids = m;
     }
     __syncthreads();
     const int n_kids = sh.n_kids;
-    const bool use_x = x != nullptr && n_kids > 0;
-    const int64_t row = int64_t(b) * a.N + cur;
-    const float* z = a.logits + row * a.ld;
-    const float* y = use_x ? a.draft + row * a.ld_draft : nullptr;
-    // the rows, kept as logits until their maxima are known
-    uint64_t top[2] = {0, 0};
-#pragma unroll 4
-    for (int i = tid; i < wk.n; i += kThreads) {
-      const float v = clean(z[wk.lo + i]);
-      w[i] = __float_as_uint(v);
-      top[0] = Max()(top[0], order_key(v, wk.lo + i));
-    }
-    if (use_x) {
-#pragma unroll 4
-      for (int i = tid; i < wk.n; i += kThreads) {
-        const float v = clean(y[wk.lo + i]);
-        x[i] = __float_as_uint(v);
-        top[1] = Max()(top[1], order_key(v, wk.lo + i));
+    const int rows = K == 2 && n_kids > 0 ? 2 : 1;
+    if (K == 2 && rows == 2) fetch(K - 1);
+    // thread j: the logits of child j's token
+    const int kid_tok = tid < n_kids ? sh.tok[sh.kid[tid]] : -1;
+    const bool kid_real = kid_tok >= 0 && kid_tok < a.V;
+    float kid_z[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) kid_z[k] = kid_real ? clean(row[k].z[kid_tok]) : 0.f;
+    uint64_t top[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      top[k] = 0;
+      if (k >= rows) continue;
+      if (T > 0.0) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) m = fmaxf(m, v[k][j]);  // (fmaxf passes over NaN)
+        top[k] = uint64_t(order_of(m)) << 32;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int i = wk.i0 + 32 * j + lane;
+          const uint64_t key = order_key(clean(v[k][j]), wk.lo + i);
+          if (j < per && i < wk.i1 && key > top[k]) top[k] = key;
+        }
       }
     }
-    wk.exchange(top, Max());
-    wk.weights(z, w, wk.over(top[0], Max()), T, top_k, top_p);
-    if (use_x) wk.weights(y, x, wk.over(top[1], Max()), T, top_k, top_p);
-    uint64_t sum[2] = {0, 0};
-    for (int i = tid; i < wk.n; i += kThreads) {
-      sum[0] += w[i];
-      if (use_x) sum[1] += x[i];
+    wk.template exchange<K, true>(top);
+    // the weights
+    uint64_t sum[K];
+    if (kCuts) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        for (int i = tid; i < kBins; i += kThreads)
+          cut[k].lo[i] = cut[k].hi[i] = cut[k].count[i] = 0;
+      __syncthreads();
     }
-    wk.exchange(sum, Add());
-    uint64_t part = sum[0];  // lane c: CTA c's share of S
-    uint64_t S = wk.over(sum[0], Add());
-    const uint64_t X = wk.over(sum[1], Add());
-    // the children's weights, from the CTAs that hold them (ordered by the
-    // exchange above)
-    for (int j = tid; j < n_kids; j += kThreads) {
-      const int t = sh.tok[sh.kid[j]];
-      uint64_t tw = 0, tx = 0;
-      if (t >= 0 && t < a.V) {
-        tw = *cl.map_shared_rank(&w[t % slice], t / slice);
-        if (use_x) tx = *cl.map_shared_rank(&x[t % slice], t / slice);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      row[k].top = top[k];
+      row[k].sum = uint64_t(kOne);  // temperature 0: the highest logit alone
+      sum[k] = 0;
+      if (k >= rows || T == 0.0) continue;
+      const float zmax = key_logit(top[k]), zmin = Exp::floor_of(zmax, a.temperature);
+      const bool inf = isinf(zmax);  // the ids at the infinite maximum alone
+      // kIlp at a time with no branch between them: the chains of dependent fp64
+      // operations overlap
+#pragma unroll
+      for (int j0 = 0; j0 < kPer; j0 += kIlp) {
+        if (j0 >= per) break;
+        double e[kIlp];
+#pragma unroll
+        for (int j = 0; j < kIlp; ++j) e[j] = ex(v[k][j0 + j], zmax, zmin);
+        if (inf) {
+#pragma unroll
+          for (int j = 0; j < kIlp; ++j)
+            e[j] = clean(v[k][j0 + j]) == zmax ? kOnes + kOne : kOnes;
+        }
+#pragma unroll
+        for (int j = 0; j < kIlp; ++j) {
+          const int i = wk.i0 + 32 * (j0 + j) + lane;
+          const uint64_t w = integer_of(e[j]);
+          if (j0 + j < per && i < wk.i1) {
+            row[k].w[i] = w;
+            sum[k] += w;
+            if (kCuts && w) {
+              const int bin = bin_of(e[j]);
+              atomicAdd(&cut[k].lo[bin], uint32_t(w & 0x3FFFF));
+              atomicAdd(&cut[k].hi[bin], uint32_t(w >> 18));
+              if (top_k > 0) atomicAdd(&cut[k].count[bin], 1u);
+            }
+          }
+        }
       }
-      sh.kw[j] = tw;
-      sh.kx[j] = tx;
     }
-    // every CTA has its copies before any weight changes
-    cl.sync();
+    if (!kCuts) {
+      if (T > 0.0) {
+        wk.template exchange<K, false>(sum);
+#pragma unroll
+        for (int k = 0; k < K; ++k) row[k].sum = sum[k];
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k >= rows) continue;
+        for (int e = wk.warp; e < kCoarse; e += kWarps) {
+          const int f = e * 32 + lane;
+          const uint64_t w = warp_add(cut[k].lo[f] + (uint64_t(cut[k].hi[f]) << 18));
+          const uint32_t m = __reduce_add_sync(kAll, cut[k].count[f]);
+          if (lane < kCluster) {
+            *wk.remote(&cut[k].in_w[rank][e], lane) = w;
+            *wk.remote(&cut[k].in_n[rank][e], lane) = m;
+          }
+        }
+        if (tid == 0) cut[k].goal = double(top_k);
+      }
+      cl.sync();
+      if (top_k > 0) {
+        wk.settle(row, rows, false, 0.0);
+        if (top_p < 1.0) {
+          if (tid < K) cut[tid].goal = top_p * double(cut[tid].kept);
+          __syncthreads();
+          wk.settle(row, rows, true, 0.0);
+        }
+      } else {
+        wk.settle(row, rows, true, top_p);
+      }
+    }
+    // the children's weights, by the same arithmetic as the rows'
+    if (tid < n_kids) {
+      uint64_t kid_w[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint64_t key = order_key(kid_z[k], kid_tok);
+        const float zmax = key_logit(row[k].top), zmin = Exp::floor_of(zmax, a.temperature);
+        if (!kid_real || k >= rows)
+          kid_w[k] = 0;
+        else if (T == 0.0)
+          kid_w[k] = key == row[k].top ? uint64_t(kOne) : 0;
+        else if (isinf(zmax))
+          kid_w[k] = kid_z[k] == zmax && key >= row[k].tau ? uint64_t(kOne) : 0;
+        else
+          kid_w[k] = key < row[k].tau ? 0 : integer_of(ex(kid_z[k], zmax, zmin));
+      }
+      sh.kw[tid] = kid_w[0];
+      sh.kx[tid] = kid_w[K - 1];
+    }
+    __syncthreads();
+    uint64_t S = row[0].sum;
+    const uint64_t X = row[K - 1].sum;
+    uint64_t* w = row[0].w;
+    const uint64_t* x = row[K - 1].w;
     int go = -1;
+    bool trimmed = !kCuts;
     for (int j = 0; j < n_kids; ++j) {
       const int c = sh.kid[j];
-      const double uc = unit(u[c]);
+      const double uc = unit(sh.u[c]);
       const uint64_t wc = sh.kw[j];
-      double f = 0.0, lhs;
-      if (use_x) {
-        f = double(S) / double(X);
-        lhs = uc * (double(sh.kx[j]) * f);
-      } else {
-        lhs = uc * double(S);
-      }
+      const double f = kDraft ? double(S) / double(X) : 0.0;
+      const double lhs = kDraft ? uc * (double(sh.kx[j]) * f) : uc * double(S);
       if (lhs < double(wc)) {
         go = c;
         break;
       }
-      if (use_x) {
+      if (T == 0.0) continue;  // the one weight stays: it is accepted or not proposed
+      if (kDraft) {
         auto less = [f](uint64_t wi, uint64_t xi) {
           const int64_t r = int64_t(wi) - __double2ll_rn(double(xi) * f);
           return r > 0 ? uint64_t(r) : uint64_t(0);
         };
-        uint64_t left[1] = {0};
-        for (int i = tid; i < wk.n; i += kThreads) left[0] += less(w[i], x[i]);
-        wk.exchange(left, Add());
-        const uint64_t total = wk.over(left[0], Add());
-        if (total) {
-          S = total;
-          part = left[0];
-          for (int i = tid; i < wk.n; i += kThreads) w[i] = less(w[i], x[i]);
+        if (!trimmed) {
+          wk.trim(row[0]);
+          wk.trim(row[K - 1]);
+          trimmed = true;
+        }
+        uint64_t left[1] = {0}, wi[kPer];
+#pragma unroll
+        for (int j1 = 0; j1 < kPer; j1 += 4) {
+          if (j1 >= per) break;
+#pragma unroll
+          for (int q = j1; q < j1 + 4; ++q) {
+            const int i = wk.i0 + 32 * q + lane;
+            wi[q] = q < per && i < wk.i1 ? less(w[i], x[i]) : 0;
+            left[0] += wi[q];
+          }
+        }
+        wk.template exchange<1, false>(left);
+        if (left[0]) {
+          S = left[0];
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            const int i = wk.i0 + 32 * q + lane;
+            if (q < per && i < wk.i1) w[i] = wi[q];
+          }
           for (int i = tid; i < n_kids; i += kThreads) sh.kw[i] = less(sh.kw[i], sh.kx[i]);
         }
       } else if (wc && S > wc) {
         const int t = sh.tok[c];
         S -= wc;
-        if (lane == t / slice) part -= wc;
-        if (rank == t / slice && tid == 0) w[t % slice] = 0;
         __syncthreads();  // every thread has read its child's weight
+        const int mine = t - wk.lo;  // by the lane that reads it in every pass
+        if (mine >= wk.i0 && mine < wk.i1 && (mine - wk.i0) % 32 == lane) w[mine] = 0;
         for (int i = tid; i < n_kids; i += kThreads)
           if (sh.tok[sh.kid[i]] == t) sh.kw[i] = 0;
       }
@@ -454,84 +688,94 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(TreeVerifyArgs a,
       __syncthreads();  // the children's list is read no more
       continue;
     }
-    // the draw from what is left
-    const double target = unit(u[0]) * double(S);
-    uint64_t incl = part;
-#pragma unroll
-    for (int o = 1; o < kMaxCluster; o <<= 1) {
-      const uint64_t yv = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += yv;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, lane < cs && part && double(incl) > target);
-    const unsigned some = __ballot_sync(0xffffffffu, lane < cs && part);
-    const int owner = past ? __ffs(int(past)) - 1 : 31 - __clz(int(some));
-    if (rank == owner) {
-      const uint64_t base = __shfl_sync(0xffffffffu, incl - part, owner);
-      // thread t: ids [t R, t R + R) of the slice
-      const int R = (wk.n + kThreads - 1) / kThreads;
-      const int i0 = min(wk.n, tid * R), i1 = min(wk.n, i0 + R);
-      if (tid == 0) sh.pick = past ? 0x7FFFFFFF : -1;
-      __syncthreads();  // also: the last changes of w
-      uint64_t s = 0;
-      int last = -1;
-      for (int i = i0; i < i1; ++i)
-        if (w[i]) {
-          s += w[i];
-          last = i;
-        }
-      uint64_t in = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t yv = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += yv;
-      }
-      if (lane == 31) sh.warp_red[0][0][wk.warp] = in;
-      __syncthreads();
-      uint64_t at = base + in - s;
-      for (int k = 0; k < wk.warp; ++k) at += sh.warp_red[0][0][k];
-      if (past) {
-        for (int i = i0; i < i1; ++i) {
-          at += w[i];
-          if (w[i] && double(at) > target) {
-            atomicMin(&sh.pick, i);
-            break;
-          }
-        }
-      } else if (last >= 0) {
-        atomicMax(&sh.pick, last);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        a.next[b] = wk.lo + sh.pick;
+    if (T == 0.0) {
+      if (rank == 0 && tid == 0) {
+        a.next[b] = int(0xFFFFFFFFu - uint32_t(row[0].top));
         a.n_path[b] = n_path;
       }
+      break;
+    }
+    // the draw from what is left: the CTA, its warp, the id (a warp's ids are
+    // consecutive)
+    const double target = unit(sh.u[0]) * double(S);
+    if (!trimmed) wk.trim(row[0]);
+    uint64_t share[1] = {0};
+#pragma unroll 4
+    for (int i = wk.i0 + lane; i < wk.i1; i += 32) share[0] += w[i];
+    const int turn = wk.turn;
+    wk.template exchange<1, false>(share);
+    uint64_t run = 0, before = 0;
+    int owner = -1, last = -1;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      const uint64_t part = sh.red[turn][0][r];
+      if (part) {
+        if (owner < 0 && double(run + part) > target) {
+          owner = r;
+          before = run;
+        }
+        last = r;
+      }
+      run += part;
+    }
+    const bool past = owner >= 0;  // else the last id that is left
+    if (!past) owner = last;
+    if (rank != owner) break;
+    const uint64_t mine = lane < kWarps ? sh.warp_red[turn][0][lane] : 0;
+    const uint64_t in = warp_scan(mine, lane);
+    const unsigned over = __ballot_sync(kAll, mine && double(before + in) > target);
+    const unsigned any = __ballot_sync(kAll, mine != 0);
+    const int ow = past ? __ffs(int(over)) - 1 : 31 - __clz(int(any));
+    if (wk.warp != ow) break;
+    run = before + __shfl_sync(kAll, in - mine, ow);
+    int pick = -1;
+    for (int base = wk.i0; base < wk.i1; base += 32) {
+      const uint64_t wi = base + lane < wk.i1 ? w[base + lane] : 0;
+      const uint64_t upto = warp_scan(wi, lane);
+      const unsigned hit = __ballot_sync(kAll, wi && (!past || double(run + upto) > target));
+      if (past && hit) {
+        pick = base + __ffs(int(hit)) - 1;
+        break;
+      }
+      if (hit) pick = base + 31 - __clz(int(hit));  // the last one so far
+      run += __shfl_sync(kAll, upto, 31);
+    }
+    if (lane == 0) {
+      a.next[b] = wk.lo + pick;
+      a.n_path[b] = n_path;
     }
     break;
   }
-  cl.sync();  // no CTA leaves while another may read its shared memory
+  // (behind the last exchange nobody touches another CTA's shared memory)
 }
 
-}  // namespace
-
-int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st) {
-  const int cs = kMaxCluster;
-  const int slice = cdiv(a.V, cs);
-  const size_t smem = size_t(slice) * sizeof(uint64_t) * (a.draft ? 2 : 1);
-  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_verify_kernel,
+template <bool kDraft, bool kCuts>
+int launch(const TreeVerifyArgs& a, cudaStream_t st) {
+  const int slice = cdiv(a.V, kCluster);
+  const size_t smem = (size_t(slice) * sizeof(uint64_t) + (kCuts ? sizeof(Cut) : 0)) * (kDraft ? 2 : 1);
+  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_verify_kernel<kDraft, kCuts>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(cs);
+  attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(cs) * unsigned(a.B));
+  cfg.gridDim = dim3(unsigned(kCluster) * unsigned(a.B));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  GPT2_CUDA_TRY(cudaLaunchKernelEx(&cfg, tree_verify_kernel, a, slice));
+  GPT2_CUDA_TRY(cudaLaunchKernelEx(&cfg, tree_verify_kernel<kDraft, kCuts>, a, slice));
   COUNT_LAUNCH(1);
   return GPT2_OK;
+}
+
+}  // namespace
+
+int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st) {
+  const bool cuts = a.temperature > 0.f && ((a.top_k > 0 && a.top_k < a.V) || a.top_p < 1.f);
+  if (a.draft) return cuts ? launch<true, true>(a, st) : launch<true, false>(a, st);
+  return cuts ? launch<false, true>(a, st) : launch<false, false>(a, st);
 }

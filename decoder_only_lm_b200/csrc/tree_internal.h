@@ -41,7 +41,7 @@ struct TreeVerifyArgs {
   int* err;
 };
 constexpr int kTreeMaxNodes = 256;
-constexpr int kTreeMaxVocab = 98304;
+constexpr int kTreeMaxVocab = 65536;
 int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st);
 
 struct KvAppendArgs {

@@ -319,7 +319,7 @@ def test_verify_matches(g, setting, V, pad, draft):
 @pytest.mark.parametrize("draft", [False, True], ids=["guess", "draft"])
 def test_verify_chain_and_sizes(g, draft):
     """Chains; vocabularies of one id, of fewer ids than CTAs, and the largest."""
-    for V, B, N in ((1, 4, 5), (2, 9, 6), (5, 30, 16), (13, 30, 256), (98304, 1, 3)):
+    for V, B, N in ((1, 4, 5), (2, 9, 6), (5, 30, 16), (13, 30, 256), (65536, 1, 3)):
         z, y, tok, par, u = make_verify(V, B, N, V, draft, tree="chain", scale=1.0)
         check_verify(g, z, tok, par, u, 1.0, 0, 1.0, draft=y)
         check_verify(g, z, tok, par, u, 0.9, 3, 0.8, draft=y)

@@ -61,7 +61,7 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
     return refuse("tree_attention: workspace too small");
   try {
     TreeAttnArgs a{qkv, ld_qkv, k_cache, v_cache, lens, parent, counts, B, N, H, Hkv, H / Hkv, D,
-                   Tc, out, ld_out, lse, static_cast<float*>(workspace), device_error_word()};
+                   Tc, out, ld_out, lse, static_cast<float*>(workspace), device_error_word(), nullptr};
     if (!a.err) return GPT2_ERR_CUDA;
     return launch_tree_attn(a, dtype == GPT2_BF16, static_cast<cudaStream_t>(stream));
   } catch (...) {

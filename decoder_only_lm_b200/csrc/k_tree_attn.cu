@@ -37,6 +37,7 @@ struct Smem {
   float p[MR * LP];
   uint32_t mask[kMaxNodes * kMaskWords];
   int up[kMaxNodes];
+  SeqDims table[kTable];
 };
 
 template <typename T, int D>
@@ -50,35 +51,17 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
   const int tid = threadIdx.x;
   const int r = tid >> 3, kk = tid & 7;  // row of the tile, lane of the row
   asm volatile("griddepcontrol.launch_dependents;");
-  bool bad = false;
-  int64_t total;
-  S::prefix(a, 0, &total, &bad);
-  if (bad && blockIdx.x == 0) atomicExch(a.err, kTreeBadInput);
-  const int64_t run = run_length(total, gridDim.x);
-  int64_t pos = blockIdx.x * run;
-  const int64_t end = min64(total, pos + run);
-  if (pos >= end) return;
-  int64_t first;
-  int b = S::find(a, pos, &first);
+  auto pieces = S::plan(a, sm.table);
+  __syncthreads();
   int mask_of = -1;  // sequence whose masks are in shared memory
   const float scale = rsqrtf(float(D)) * kLog2e;
   const T* qkv = static_cast<const T*>(a.qkv);
 
-  while (pos < end) {
-    const SeqDims s = seq_dims(a, b);
-    const int64_t seq_tiles = S::tiles(a, s);
-    if (pos >= first + seq_tiles) {
-      first += seq_tiles;
-      ++b;
-      continue;
-    }
-    // the piece of one segment that falls into this run
-    const int kt = S::key_tiles(s), rts = S::row_tiles(a, s), ct = S::cache_tiles(s);
-    const int seg = int((pos - first) / kt);
-    const int64_t s0 = first + int64_t(seg) * kt;
-    const int hk = seg / rts, rt = seg % rts;
-    const int t0 = int(pos - s0), t1 = int(min64(kt, end - s0));
-    const int rows = min(MR, s.n * a.G - rt * MR);
+  Piece p;
+  while (pieces.next(p)) {
+    const SeqDims s{p.len, p.n};
+    const int b = p.b, hk = p.hk, rt = p.rt, t0 = p.t0, t1 = p.t1, ct = p.ct, rows = p.rows;
+    if (tid == 0 && t0 == 0) pieces.note(p);
     const T* xb = qkv + int64_t(b) * a.N * a.ld_qkv;  // this sequence's nodes
     __syncthreads();  // the previous piece is done with shared memory
     for (int e = tid; e < MR * V4; e += kThreads) {
@@ -92,7 +75,8 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
       *reinterpret_cast<float4*>(&sm.q[rr * LD + c * 4]) = f;
     }
     if (t1 > ct && mask_of != b) {
-      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, sm.mask, sm.up, a.err);
+      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, sm.mask, sm.up, a.err, tid, kThreads,
+                  [] { __syncthreads(); });
       mask_of = b;
     }
     const int node = r < rows ? (rt * MR + r) / a.G : 0;
@@ -164,9 +148,9 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float p = exp2f(sc[j] - base);
-          sum += p;
-          sm.p[r * LP + kk + 8 * j] = p;
+          const float pj = exp2f(sc[j] - base);
+          sum += pj;
+          sm.p[r * LP + kk + 8 * j] = pj;
         }
 #pragma unroll
         for (int x = 1; x < 8; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -197,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
       __syncthreads();
     }
 
-    if (t0 == 0 && t1 == kt) {  // the whole segment: finished here
+    if (p.whole()) {  // finished here
       if (r < rows) {
         const int gr = rt * MR + r, h = hk * a.G + gr % a.G;
         T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + node) * a.ld_out + int64_t(h) * D;
@@ -216,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
           a.lse[(int64_t(b) * a.H + h) * a.N + node] = (m + log2f(l)) * kLn2;
       }
     } else {
-      float* w = a.ws + slot_of(blockIdx.x, s0, run) * slot_floats<MR>(D);
+      float* w = a.ws + pieces.slot(p) * slot_floats<MR>(D);
       if (r < rows) {
 #pragma unroll
         for (int j = 0; j < NO; ++j)
@@ -227,7 +211,6 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
         }
       }
     }
-    pos = s0 + t1;
   }
 }
 
@@ -239,10 +222,11 @@ int launch_simt(const TreeAttnArgs& a, cudaStream_t st) {
   GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_simt_kernel<T, D>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const int grid = simt_grid();
-  tree_attn_simt_kernel<T, D><<<grid, kThreads, smem, st>>>(a);
+  const TreeAttnArgs w = with_workspace<MR>(a, grid);
+  tree_attn_simt_kernel<T, D><<<grid, kThreads, smem, st>>>(w);
   COUNT_LAUNCH(1);
   GPT2_LAUNCH_CHECK();
-  return launch_combine<T, MR, KT>(a, grid, st);
+  return launch_combine<T, MR, D>(w, st);
 }
 
 template <typename T>
@@ -257,14 +241,26 @@ int launch_simt_d(const TreeAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t tree_attn_mma_workspace(int N, int H, int Hkv, int D);
+size_t tree_attn_mma_workspace(int B, int N, int H, int Hkv, int D);
 int launch_tree_attn_mma(const TreeAttnArgs& a, cudaStream_t st);
+size_t tree_attn_tc_workspace(int B, int N, int H, int Hkv, int D);
+int launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t st);
+
+// bf16 with head size 64 or 128 and more than kFewRows query rows per
+// key/value head: 5th-generation tensor cores.
+#include <cstdlib>
+static bool on_tc(int N, int H, int Hkv, int D) {
+  static const int kFewRows = getenv("TA_ROWS") ? atoi(getenv("TA_ROWS")) : 16;
+  return D >= 64 && N * (H / Hkv) > kFewRows;
+}
 
 size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16_in) {
-  return bf16_in ? tree_attn_mma_workspace(N, H, Hkv, D)
-                 : size_t(2) * simt_grid() * slot_floats<MR>(D) * sizeof(float);
+  if (!bf16_in) return workspace_bytes<MR>(simt_grid(), B, N, H, Hkv, D);
+  return on_tc(N, H, Hkv, D) ? tree_attn_tc_workspace(B, N, H, Hkv, D)
+                             : tree_attn_mma_workspace(B, N, H, Hkv, D);
 }
 
 int launch_tree_attn(const TreeAttnArgs& a, int bf16_in, cudaStream_t st) {
-  return bf16_in ? launch_tree_attn_mma(a, st) : launch_simt_d<float>(a, st);
+  if (!bf16_in) return launch_simt_d<float>(a, st);
+  return on_tc(a.N, a.H, a.Hkv, a.D) ? launch_tree_attn_tc(a, st) : launch_tree_attn_mma(a, st);
 }

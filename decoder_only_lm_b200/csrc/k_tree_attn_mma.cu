@@ -38,7 +38,7 @@ struct Cfg {
   static constexpr int LO = D + 4;            // row stride of the merge buffer
   static constexpr int kMerge = WK > 1 ? WK * MR * (LO + 2) * 4 : 0;
   static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kSmem = kBuf + kMaxNodes * (kMaskWords + 1) * 4 + 16;
+  static constexpr int kSmem = kBuf + kMaxNodes * (kMaskWords + 1) * 4 + 16 + kTable * 8;
   static constexpr int kCtas = WM == 8 ? (D == 128 ? 1 : 2) : D == 128 ? 2 : 3;  // per SM
 };
 
@@ -113,38 +113,22 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
   uint32_t* mask = reinterpret_cast<uint32_t*>(buf + F::kBuf);
   int* up = reinterpret_cast<int*>(mask + kMaxNodes * kMaskWords);
   uint32_t* odd = reinterpret_cast<uint32_t*>(up + kMaxNodes);  // 64 bits: keys of non-finite V
+  SeqDims* table = reinterpret_cast<SeqDims*>(odd + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % WM, wk = warp / WM;
   const int gr = lane >> 2, gc = lane & 3;  // fragment row and column pair
   asm volatile("griddepcontrol.launch_dependents;");
-  bool bad = false;
-  int64_t total;
-  S::prefix(a, 0, &total, &bad);
-  if (bad && blockIdx.x == 0) atomicExch(a.err, kTreeBadInput);
-  const int64_t run = run_length(total, gridDim.x);
-  int64_t pos = blockIdx.x * run;
-  const int64_t end = min64(total, pos + run);
-  if (pos >= end) return;
-  int64_t first;
-  int b = S::find(a, pos, &first);
+  auto pieces = S::plan(a, table);
+  __syncthreads();
   int mask_of = -1;
   const float scale = rsqrtf(float(D)) * kLog2e;
   const bf16* qkv = static_cast<const bf16*>(a.qkv);
 
-  while (pos < end) {
-    const SeqDims s = seq_dims(a, b);
-    const int64_t seq_tiles = S::tiles(a, s);
-    if (pos >= first + seq_tiles) {
-      first += seq_tiles;
-      ++b;
-      continue;
-    }
-    const int kt = S::key_tiles(s), rts = S::row_tiles(a, s), ct = S::cache_tiles(s);
-    const int seg = int((pos - first) / kt);
-    const int64_t s0 = first + int64_t(seg) * kt;
-    const int hk = seg / rts, rt = seg % rts;
-    const int t0 = int(pos - s0), t1 = int(min64(kt, end - s0));
-    const int rows = min(MR, s.n * a.G - rt * MR);
+  Piece pc;
+  while (pieces.next(pc)) {
+    const SeqDims s{pc.len, pc.n};
+    const int b = pc.b, hk = pc.hk, rt = pc.rt, t0 = pc.t0, t1 = pc.t1, ct = pc.ct, rows = pc.rows;
+    if (tid == 0 && t0 == 0) pieces.note(pc);
     const bf16* xb = qkv + int64_t(b) * a.N * a.ld_qkv;
     const bf16* kc = static_cast<const bf16*>(a.k) + (int64_t(b) * a.Hkv + hk) * a.Tc * D;
     const bf16* vc = static_cast<const bf16*>(a.v) + (int64_t(b) * a.Hkv + hk) * a.Tc * D;
@@ -198,7 +182,8 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
       }
     }
     if (t1 > ct && mask_of != b) {
-      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, mask, up, a.err);
+      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, mask, up, a.err, tid, F::kThreads,
+                  [] { __syncthreads(); });
       mask_of = b;
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -365,8 +350,8 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       m[h] = __fmul_rn(m[h], scale);  // log2 domain, the base of the sums
     }
-    const bool whole = t0 == 0 && t1 == kt;
-    float* w = a.ws + slot_of(blockIdx.x, s0, run) * slot_floats<MR>(D);
+    const bool whole = pc.whole();
+    float* w = a.ws + pieces.slot(pc) * slot_floats<MR>(D);
     bf16* out = static_cast<bf16*>(a.out) + int64_t(b) * a.N * a.ld_out;
     if (WK == 1) {
 #pragma unroll
@@ -444,7 +429,6 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         }
       }
     }
-    pos = s0 + t1;
   }
 }
 
@@ -452,14 +436,14 @@ template <int D, int WM, int WK>
 struct Variant {
   using F = Cfg<D, WM, WK>;
   static int grid() { return F::kCtas * gpt2_internal::sm_count(); }
-  static size_t workspace() { return size_t(2) * grid() * slot_floats<F::MR>(D) * sizeof(float); }
   static int launch(const TreeAttnArgs& a, cudaStream_t st) {
     GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_mma_kernel<D, WM, WK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem));
-    tree_attn_mma_kernel<D, WM, WK><<<grid(), F::kThreads, F::kSmem, st>>>(a);
+    const TreeAttnArgs w = with_workspace<F::MR>(a, grid());
+    tree_attn_mma_kernel<D, WM, WK><<<grid(), F::kThreads, F::kSmem, st>>>(w);
     COUNT_LAUNCH(1);
     GPT2_LAUNCH_CHECK();
-    return launch_combine<bf16, F::MR, KT>(a, grid(), st);
+    return launch_combine<bf16, F::MR, D>(w, st);
   }
 };
 
@@ -485,8 +469,11 @@ auto pick(int D, int rows, Fn fn) {
 
 }  // namespace
 
-size_t tree_attn_mma_workspace(int N, int H, int Hkv, int D) {
-  return pick(D, N * (H / Hkv), [](auto v) { return decltype(v)::workspace(); });
+size_t tree_attn_mma_workspace(int B, int N, int H, int Hkv, int D) {
+  return pick(D, N * (H / Hkv), [&](auto v) {
+    using V = decltype(v);
+    return workspace_bytes<V::F::MR>(V::grid(), B, N, H, Hkv, D);
+  });
 }
 
 int launch_tree_attn_mma(const TreeAttnArgs& a, cudaStream_t st) {

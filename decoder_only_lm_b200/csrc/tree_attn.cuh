@@ -43,12 +43,22 @@ __device__ __forceinline__ SeqDims seq_dims(const TreeAttnArgs& a, int b, bool* 
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+constexpr int kTable = 32;  // sequences whose lengths a CTA keeps in shared memory
+
+// One piece of a CTA's run: key tiles [t0, t1) of a segment.
+struct Piece {
+  int b, hk, rt, t0, t1;
+  int len, n, rows;  // the sequence's lengths, real rows of the row tile
+  int kt, ct;        // key tiles of the segment, of them cache tiles
+  int64_t s0;        // the segment's first tile in the list
+  __device__ bool whole() const { return t0 == 0 && t1 == kt; }
+};
+
 template <int MR, int KT>
 struct Split {
   __device__ static int row_tiles(const TreeAttnArgs& a, SeqDims s) {
     return ceil_div(s.n * a.G, MR);
   }
-  __device__ static int cache_tiles(SeqDims s) { return ceil_div(s.len, KT); }
   // key tiles of each segment of the sequence (0 when it has no node)
   __device__ static int key_tiles(SeqDims s) {
     return s.n ? ceil_div(s.len, KT) + ceil_div(s.n, KT) : 0;
@@ -56,67 +66,123 @@ struct Split {
   __device__ static int64_t tiles(const TreeAttnArgs& a, SeqDims s) {
     return int64_t(a.Hkv) * row_tiles(a, s) * key_tiles(s);
   }
-  // Tiles before sequence `upto`, and over all; by every warp on its own.
-  __device__ static int64_t prefix(const TreeAttnArgs& a, int upto, int64_t* total, bool* bad) {
-    const int lane = threadIdx.x & 31;
-    int64_t before = 0, all = 0;
-    for (int b = lane; b < a.B; b += 32) {
-      const int64_t t = tiles(a, seq_dims(a, b, bad));
-      all += t;
-      if (b < upto) before += t;
+
+  // The pieces of a CTA's run in order.
+  struct Pieces {
+    const TreeAttnArgs& a;
+    const SeqDims* table;  // lengths of sequences b0 .. b0 + 31
+    int64_t pos, end, run, first;
+    int b0, b;
+    __device__ bool next(Piece& p) {
+      while (pos < end) {
+        const SeqDims s = b - b0 < kTable ? table[b - b0] : seq_dims(a, b);
+        const int64_t n = tiles(a, s);
+        if (pos >= first + n) {
+          first += n;
+          ++b;
+          continue;
+        }
+        p.b = b;
+        p.len = s.len;
+        p.n = s.n;
+        p.kt = key_tiles(s);
+        p.ct = ceil_div(s.len, KT);
+        const int rts = row_tiles(a, s);
+        const int seg = n < (int64_t(1) << 31) ? int(uint32_t(pos - first) / uint32_t(p.kt))
+                                               : int((pos - first) / p.kt);
+        p.s0 = first + int64_t(seg) * p.kt;
+        p.hk = seg / rts;
+        p.rt = seg % rts;
+        p.t0 = int(pos - p.s0);
+        p.t1 = int(min64(p.kt, end - p.s0));
+        p.rows = min(MR, s.n * a.G - p.rt * MR);
+        pos = p.s0 + p.t1;
+        return true;
+      }
+      return false;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
+    // Workspace slot of a piece that is not a whole segment: 2 per CTA, the first
+    // for a segment that began before the run, the second for one that begins
+    // in it and goes on.
+    __device__ int64_t slot(const Piece& p) const { return 2 * int64_t(blockIdx.x) + (p.t0 == 0); }
+    // By the CTA in whose run the segment begins: the first and last CTA that
+    // hold a piece of it.
+    __device__ void note(const Piece& p) const {
+      const int rts = ceil_div(a.N * a.G, MR);
+      a.seg[(int64_t(p.b) * a.Hkv + p.hk) * rts + p.rt] =
+          make_int2(int(blockIdx.x), p.whole() ? int(blockIdx.x) : int((p.s0 + p.kt - 1) / run));
     }
-    *total = all;
-    return before;
-  }
-  // Sequence that holds tile `pos` (< total), and the tiles before it.
-  __device__ static int find(const TreeAttnArgs& a, int64_t pos, int64_t* first) {
+  };
+
+  // This CTA's run; every warp on its own, the table filled by the caller's
+  // first warp (a block barrier must follow).
+  __device__ static Pieces plan(const TreeAttnArgs& a, SeqDims* table) {
     const int lane = threadIdx.x & 31;
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t t = b < a.B ? tiles(a, seq_dims(a, b)) : 0;
-      int64_t incl = t;
+    const bool fill = threadIdx.x < 32;
+    bool bad = false;
+    int64_t total = 0, first = 0, base = 0;
+    int b0 = a.B;
+    Pieces q{a, table, 0, 0, 1, 0, 0, 0};
+    auto scan = [&](int64_t v) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + incl > pos);
+      return v;
+    };
+    SeqDims s{0, 0};
+    int64_t t = 0, in = 0;
+    for (int c = 0; c < a.B; c += 32) {
+      s = c + lane < a.B ? seq_dims(a, c + lane, &bad) : SeqDims{0, 0};
+      t = tiles(a, s);
+      in = scan(t);
+      total += __shfl_sync(0xffffffffu, in, 31);
+    }
+    if (bad && blockIdx.x == 0) atomicExch(a.err, kTreeBadInput);
+    q.run = total > 0 ? (total + gridDim.x - 1) / gridDim.x : 1;
+    q.pos = blockIdx.x * q.run;
+    q.end = min64(total, q.pos + q.run);
+    if (q.pos >= q.end) {
+      q.end = q.pos;
+      return q;
+    }
+    for (int c = 0; c < a.B; c += 32) {
+      if (a.B > 32) {  // (else the lane's values are those of the loop above)
+        s = c + lane < a.B ? seq_dims(a, c + lane) : SeqDims{0, 0};
+        t = tiles(a, s);
+        in = scan(t);
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + in > q.pos);
       if (hit) {
         const int src = __ffs(int(hit)) - 1;
-        *first = base + __shfl_sync(0xffffffffu, incl - t, src);
-        return b0 + src;
+        first = base + __shfl_sync(0xffffffffu, in - t, src);
+        b0 = c + src;
+        if (fill) {
+          if (lane >= src) table[lane - src] = s;
+          // the rest of the table (b0 .. b0 + 31) when the batch goes on
+          const int more = c + 32 + lane;
+          if (lane < src && more < a.B) table[more - b0] = seq_dims(a, more);
+        }
+        break;
       }
-      base += __shfl_sync(0xffffffffu, incl, 31);
+      base += __shfl_sync(0xffffffffu, in, 31);
     }
-    *first = base;
-    return a.B;
+    q.first = first;
+    q.b0 = q.b = b0;
+    return q;
   }
 };
 
-// Tiles of every CTA's run.
-__device__ __forceinline__ int64_t run_length(int64_t total, int grid) {
-  return total > 0 ? (total + grid - 1) / grid : 1;
-}
-
-// Partial slot of CTA c for a segment that starts at tile s0: 0 for a segment
-// that began before the CTA's run, 1 for one that begins in it and goes on.
-__device__ __forceinline__ int64_t slot_of(int64_t c, int64_t s0, int64_t run) {
-  return 2 * c + (s0 >= c * run ? 1 : 0);
-}
-
 // Ancestor masks of the sequence's nodes, bit j of mask i: node j is on the
 // path from node i to the root, i included.  Doubling: mask(i) |= mask(up(i)),
-// up(i) = up(up(i)); ceil(log2 n) rounds for a chain of n.  All threads of the
-// block.  A parent outside [-1, i) counts as -1 and is reported.
+// up(i) = up(up(i)); ceil(log2 n) rounds for a chain of n.  By the
+// `threads` threads that call it (>= kMaxNodes / 2; thread tid of them), with
+// `sync` their barrier.  A parent outside [-1, i) counts as -1 and is reported.
+template <typename Sync>
 __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32_t* mask, int* up,
-                                            int* err) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+                                            int* err, int tid, int threads, Sync sync) {
+  for (int i = tid; i < n; i += threads) {
     int p = parent ? parent[i] : i - 1;
     if (p < -1 || p >= i) {
       atomicExch(err, kTreeBadInput);
@@ -126,14 +192,14 @@ __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32
 #pragma unroll
     for (int w = 0; w < kMaskWords; ++w) mask[i * kMaskWords + w] = (i >> 5) == w ? 1u << (i & 31) : 0;
   }
-  __syncthreads();
+  sync();
   for (int reach = 1; reach < n; reach <<= 1) {
-    // reads of this round, then its writes (n <= kMaxNodes <= 2 blockDim.x)
+    // reads of this round, then its writes
     uint32_t add[2][kMaskWords];
     int nu[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
+      const int i = tid + k * threads;
       nu[k] = -1;
       if (i < n && up[i] >= 0) {
         nu[k] = up[up[i]];
@@ -144,100 +210,120 @@ __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32
         for (int w = 0; w < kMaskWords; ++w) add[k][w] = 0;
       }
     }
-    __syncthreads();
+    sync();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
+      const int i = tid + k * threads;
       if (i < n) {
         up[i] = nu[k];
 #pragma unroll
         for (int w = 0; w < kMaskWords; ++w) mask[i * kMaskWords + w] |= add[k][w];
       }
     }
-    __syncthreads();
+    sync();
   }
 }
 
 // Workspace: 2 slots per CTA, each MR x D fp32 outputs, then the rows' running
-// maximum and sum (log2 domain), MR of each.
+// maximum (log2 domain) and sum, MR of each; then the segments' first and last
+// CTA.
 template <int MR>
 __host__ __device__ inline int64_t slot_floats(int D) {
   return int64_t(MR) * (D + 2);
 }
+template <int MR>
+size_t workspace_bytes(int grid, int B, int N, int H, int Hkv, int D) {
+  return size_t(2) * grid * slot_floats<MR>(D) * sizeof(float) +
+         size_t(B) * Hkv * cdiv(N * (H / Hkv), MR) * sizeof(int2);
+}
+template <int MR>
+TreeAttnArgs with_workspace(TreeAttnArgs a, int grid) {
+  a.seg = reinterpret_cast<int2*>(a.ws + 2 * int64_t(grid) * slot_floats<MR>(a.D));
+  return a;
+}
 
-// One warp (WPR = 1) or one block of WPR warps per query row: the pieces of a
-// split segment merged in order,
-//   M = max m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
-template <typename T, int MR, int KT, int WPR>
-__global__ void __launch_bounds__(128) tree_combine_kernel(TreeAttnArgs a, int grid) {
-  using S = Split<MR, KT>;
-  constexpr int RPB = 4 / WPR;  // rows of a block
+// The pieces of a split segment merged in order,
+//   M = max m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,
+// by WPR warps per query row (1 or 4).  D / 4 lanes cover a row with 16-byte
+// loads, so 128 / D pieces of a warp are in flight at once.
+template <typename T, int MR, int D, int WPR>
+__global__ void __launch_bounds__(128) tree_combine_kernel(TreeAttnArgs a) {
+  constexpr int RPB = 4 / WPR;   // rows of a block
+  constexpr int LP = D / 4;      // lanes of a piece's row
+  constexpr int GP = 32 / LP;    // pieces at once
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float sh_o[WPR > 1 ? 4 : 1][WPR > 1 ? 128 : 1];
-  __shared__ float sh_l[4];
+  __shared__ float4 sh_o[WPR > 1 ? 4 : 1][WPR > 1 ? LP : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int R = a.N * a.G;  // rows of a (sequence, key/value head)
-  const int64_t row = int64_t(blockIdx.x) * RPB + (WPR > 1 ? 0 : warp);
-  if (row >= int64_t(a.B) * a.Hkv * R) return;  // WPR > 1: whole block
-  const int r = int(row % R), hk = int(row / R % a.Hkv), b = int(row / R / a.Hkv);
-  const SeqDims s = seq_dims(a, b);
-  if (r >= s.n * a.G) return;
-  int64_t total;
-  const int64_t first = S::prefix(a, b, &total, nullptr);
-  const int64_t run = run_length(total, grid);
-  const int kt = S::key_tiles(s);
-  const int64_t s0 = first + (int64_t(hk) * S::row_tiles(a, s) + r / MR) * kt, s1 = s0 + kt;
-  const int64_t c0 = s0 / run, c1 = (s1 - 1) / run;
-  if (c0 == c1) return;  // finished by its CTA
-  const int rr = r % MR, D = a.D;
+  const uint32_t R = uint32_t(a.N) * a.G;  // rows of a (sequence, key/value head)
+  const uint32_t row = blockIdx.x * RPB + (WPR > 1 ? 0 : warp);
+  if (row >= uint32_t(a.B) * a.Hkv * R) return;  // WPR > 1: whole block
+  const int r = int(row % R), bh = int(row / R), b = bh / a.Hkv, hk = bh % a.Hkv;
+  const int2 seg = a.seg[int64_t(bh) * ceil_div(int(R), MR) + r / MR];
+  if (r >= seq_dims(a, b).n * a.G) return;
+  const int np = seg.y - seg.x + 1;  // the first in its CTA's second slot
+  if (np == 1) return;               // finished by its CTA
   const int64_t sf = slot_floats<MR>(D);
+  const int rr = r % MR;
+  auto piece = [&](int i) { return a.ws + (2 * int64_t(seg.x + i) + (i == 0)) * sf; };
   float M = -INFINITY;
-  for (int64_t c = c0 + lane; c <= c1; c += 32)
-    M = fmaxf(M, a.ws[slot_of(c, s0, run) * sf + int64_t(MR) * D + rr]);
+  for (int i = lane; i < np; i += 32) M = fmaxf(M, piece(i)[MR * D + rr]);
   M = warp_max(M);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
   const int sub = WPR > 1 ? warp : 0;
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  for (int64_t c = c0 + sub; c <= c1; c += WPR) {
-    const float* p = a.ws + slot_of(c, s0, run) * sf;
-    const float m = p[int64_t(MR) * D + rr];
+#pragma unroll 4
+  for (int i = sub * GP + lane / LP; i < np; i += WPR * GP) {
+    const float* p = piece(i);
+    const float m = p[MR * D + rr];
     const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-    l = fmaf(w, p[int64_t(MR) * D + MR + rr], l);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int d = lane + 32 * k;
-      if (d < D) o[k] = fmaf(w, p[int64_t(rr) * D + d], o[k]);
-    }
+    const float4 x = *reinterpret_cast<const float4*>(p + int64_t(rr) * D + lane % LP * 4);
+    o.x = fmaf(w, x.x, o.x);
+    o.y = fmaf(w, x.y, o.y);
+    o.z = fmaf(w, x.z, o.z);
+    o.w = fmaf(w, x.w, o.w);
   }
+#pragma unroll
+  for (int x = LP; x < 32; x <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+  }
+  for (int i = lane; i < np; i += 32) {
+    const float* p = piece(i);
+    const float m = p[MR * D + rr];
+    l = fmaf(m == -INFINITY ? 0.f : exp2f(m - M), p[MR * D + MR + rr], l);
+  }
+  l = warp_sum(l);
   if (WPR > 1) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (lane + 32 * k < D) sh_o[warp][lane + 32 * k] = o[k];
-    if (lane == 0) sh_l[warp] = l;
+    if (lane < LP) sh_o[warp][lane] = o;
     __syncthreads();
-    if (warp) return;
-    l = 0.f;
-    for (int w = 0; w < WPR; ++w) l += sh_l[w];
+    if (warp || lane >= LP) return;
+    o = sh_o[0][lane];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[k] = 0.f;
-      if (lane + 32 * k < D)
-        for (int w = 0; w < WPR; ++w) o[k] += sh_o[w][lane + 32 * k];
+    for (int w = 1; w < 4; ++w) {
+      const float4 x = sh_o[w][lane];
+      o.x += x.x;
+      o.y += x.y;
+      o.z += x.z;
+      o.w += x.w;
     }
   }
+  if (lane >= LP) return;
   const int i = r / a.G, h = hk * a.G + r % a.G;
-  T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + i) * a.ld_out + int64_t(h) * D;
+  T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + i) * a.ld_out + int64_t(h) * D + lane * 4;
   const float inv = 1.f / l;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (lane + 32 * k < D) out[lane + 32 * k] = from_f32<T>(o[k] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(int64_t(b) * a.H + h) * a.N + i] = (M + log2f(l)) * kLn2;
+  out[0] = from_f32<T>(o.x * inv);
+  out[1] = from_f32<T>(o.y * inv);
+  out[2] = from_f32<T>(o.z * inv);
+  out[3] = from_f32<T>(o.w * inv);
+  if (a.lse && lane == 0) a.lse[(int64_t(b) * a.H + h) * a.N + i] = (M + log2f(l)) * kLn2;
 }
 
 // Launched with programmatic serialisation: its blocks may be resident before
 // the attention kernel ends and wait for it on the device.
-template <typename T, int MR, int KT>
-int launch_combine(const TreeAttnArgs& a, int grid, cudaStream_t st) {
+template <typename T, int MR, int D>
+int launch_combine(const TreeAttnArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.B) * a.N * a.H;
   // few rows: each has many pieces, four warps share them
   const bool wide = rows < 8 * int64_t(gpt2_internal::sm_count());
@@ -250,8 +336,8 @@ int launch_combine(const TreeAttnArgs& a, int grid, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  GPT2_CUDA_TRY(wide ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, KT, 4>, a, grid)
-                     : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, KT, 1>, a, grid));
+  GPT2_CUDA_TRY(wide ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, D, 4>, a)
+                     : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, D, 1>, a));
   COUNT_LAUNCH(1);
   return GPT2_OK;
 }

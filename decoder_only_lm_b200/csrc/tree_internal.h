@@ -21,6 +21,7 @@ struct TreeAttnArgs {
   float* lse;
   float* ws;
   int* err;
+  int2* seg;  // in the workspace, set by the launchers
 };
 
 size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16);

@@ -143,6 +143,18 @@ def test_attention_sizes(g, dtype, B, N, H, Hkv, D, lens, tree):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_many_pieces_a_cta(g, dtype, D):
+    """Short segments, several of them in every CTA's run, each ending in a
+    partly filled tile and the nodes' own."""
+    lens = [(37 * b) % 911 for b in range(24)]
+    c = Case(dtype, 24, 20, 24, 12, D, 911, lens, seed=D, tree="random",
+             counts=[1 + (7 * b) % 20 for b in range(24)])
+    c.check(*c.call(g))
+    assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("D", [16, 64, 128])
 @pytest.mark.parametrize("N", [6, 40])
 def test_attention_peaked_rows(g, dtype, D, N):

@@ -35,9 +35,10 @@ struct Smem {
   float k[KT * LD];
   float v[KT * LD];
   float p[MR * LP];
-  uint32_t mask[kMaxNodes * kMaskWords];
+  alignas(16) uint32_t mask[kMaxNodes * kMaskWords];
   int up[kMaxNodes];
   SeqDims table[kTable];
+  uint32_t flag;
 };
 
 template <typename T, int D>
@@ -74,8 +75,8 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
       }
       *reinterpret_cast<float4*>(&sm.q[rr * LD + c * 4]) = f;
     }
-    if (t1 > ct && mask_of != b) {
-      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, sm.mask, sm.up, a.err, tid, kThreads,
+    if (a.parent && t1 > ct && mask_of != b) {
+      build_masks(a.parent + int64_t(b) * a.N, s.n, sm.mask, sm.up, &sm.flag, a.err, tid, kThreads,
                   [] { __syncthreads(); });
       mask_of = b;
     }
@@ -129,15 +130,11 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
           }
         }
         float mx = m;
+        const uint64_t see = fresh ? sees(!a.parent, sm.mask, node, k0) : ~uint64_t(0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int key = kk + 8 * j;
-          bool see = key < nk;
-          if (fresh && see) {
-            const int kn = k0 + key;
-            see = (sm.mask[node * kMaskWords + (kn >> 5)] >> (kn & 31)) & 1;
-          }
-          if (!see) sc[j] = -INFINITY;
+          if (key >= nk || !((see >> key) & 1)) sc[j] = -INFINITY;
           mx = fmaxf(mx, sc[j]);
         }
 #pragma unroll

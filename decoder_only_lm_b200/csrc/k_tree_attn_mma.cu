@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         q[k][2 + h] = real ? *reinterpret_cast<const uint32_t*>(p + 16 * k + 8) : 0u;
       }
     }
-    if (t1 > ct && mask_of != b) {
-      build_masks(a.parent ? a.parent + int64_t(b) * a.N : nullptr, s.n, mask, up, a.err, tid, F::kThreads,
+    if (a.parent && t1 > ct && mask_of != b) {
+      build_masks(a.parent + int64_t(b) * a.N, s.n, mask, up, odd + 2, a.err, tid, F::kThreads,
                   [] { __syncthreads(); });
       mask_of = b;
     }
@@ -257,17 +257,17 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         }
       }
       if (fresh || nk < KW) {
+        uint64_t see[2] = {~uint64_t(0), ~uint64_t(0)};
+        if (fresh) {
+          see[0] = sees(!a.parent, mask, node[0], k0) >> (wk * KW);
+          see[1] = sees(!a.parent, mask, node[1], k0) >> (wk * KW);
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = j * 8 + gc * 2 + (e & 1);
-            bool see = key < nk;
-            if (fresh) {
-              const int kk = k0 + wk * KW + key;
-              see = see && ((mask[node[e >> 1] * kMaskWords + (kk >> 5)] >> (kk & 31)) & 1);
-            }
-            if (!see) sc[j][e] = -INFINITY;
+            if (key >= nk || !((see[e >> 1] >> key) & 1)) sc[j][e] = -INFINITY;
           }
       }
       // running maximum (log2 domain: s scale), probabilities, sums

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto b_od = [&](int i) { return smem_u32(bars + 7 + 2 * NS + i); };
   const uint32_t b_rows = smem_u32(bars + 9 + 2 * NS);
   uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10 + 2 * NS);
-  SeqDims* table = reinterpret_cast<SeqDims*>(slot + 4);
+  SeqDims* table = reinterpret_cast<SeqDims*>(slot + 6);
   uint32_t* odd = slot + 1;  // keys of a node tile whose values are not finite
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -282,9 +282,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool busy = ((warp & 3) * 32) < p.rows;
       const int gr = p.rt * MR + (real ? e : 0), node = gr / a.G, hq = p.hk * a.G + gr % a.G;
       if (e == 0 && p.t0 == 0) pieces.note(p);
-      if (p.t1 > p.ct && mask_of != p.b) {
-        build_masks(a.parent ? a.parent + int64_t(p.b) * a.N : nullptr, p.n, mask, up, a.err, e, 128,
-                    rows_sync);
+      if (a.parent && p.t1 > p.ct && mask_of != p.b) {
+        build_masks(a.parent + int64_t(p.b) * a.N, p.n, mask, up, odd + 2, a.err, e, 128, rows_sync);
         mask_of = p.b;
       }
       float m = -INFINITY, l = 0.f;
@@ -319,10 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const bool fresh = t >= p.ct;
           const int k0 = (fresh ? t - p.ct : t) * KT, nk = (fresh ? p.n : p.len) - k0;
           uint64_t see = nk >= KT ? ~uint64_t(0) : (uint64_t(1) << nk) - 1;
-          if (fresh) {
-            const uint32_t* w = mask + node * kMaskWords + (k0 >> 5);
-            see &= w[0] | (uint64_t(w[1]) << 32);
-          }
+          if (fresh) see &= sees(!a.parent, mask, node, k0);
 #pragma unroll
           for (int i = 0; i < 64; ++i) x[i] = (see >> i) & 1 ? x[i] : -INFINITY;
         }

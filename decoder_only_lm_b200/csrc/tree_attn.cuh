@@ -6,9 +6,10 @@
 // key/value head), cut into row tiles of MR rows; its keys are the cached
 // positions followed by the nodes, each cut into key tiles of KT.  A segment is
 // one (b, key/value head, row tile); the key tiles of all segments, in that
-// order, form one list, and every CTA takes an equal run of consecutive tiles,
-// whatever the lengths are: a long sequence is split over many CTAs, short ones
-// share one.  Lengths are read on the device, so a recorded launch follows
+// order, form one list, and every CTA takes an equal run of it, whatever the
+// lengths are: a long sequence is split over many CTAs, short ones share one.
+// Each segment counts kExtra tiles more than it has, for what a piece costs
+// besides its tiles (queries, masks, results).  Lengths are read on the device, so a recorded launch follows
 // them.  A segment inside one CTA's run is finished there; the pieces of any
 // other go to the workspace (unnormalised output, running maximum and sum in
 // fp32) and tree_combine_kernel merges them in tile order, so the result does
@@ -43,6 +44,7 @@ __device__ __forceinline__ SeqDims seq_dims(const TreeAttnArgs& a, int b, bool* 
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+constexpr int kExtra = 2;
 constexpr int kTable = 32;  // sequences whose lengths a CTA keeps in shared memory
 
 // One piece of a CTA's run: key tiles [t0, t1) of a segment.
@@ -63,15 +65,17 @@ struct Split {
   __device__ static int key_tiles(SeqDims s) {
     return s.n ? ceil_div(s.len, KT) + ceil_div(s.n, KT) : 0;
   }
+  // places in the list
   __device__ static int64_t tiles(const TreeAttnArgs& a, SeqDims s) {
-    return int64_t(a.Hkv) * row_tiles(a, s) * key_tiles(s);
+    return s.n ? int64_t(a.Hkv) * row_tiles(a, s) * (key_tiles(s) + kExtra) : 0;
   }
 
   // The pieces of a CTA's run in order.
   struct Pieces {
     const TreeAttnArgs& a;
     const SeqDims* table;  // lengths of sequences b0 .. b0 + 31
-    int64_t pos, end, run, first;
+    int64_t pos, end, total, first;
+    int ctas;  // CTAs with a run: never more than places, so that none is empty
     int b0, b;
     __device__ bool next(Piece& p) {
       while (pos < end) {
@@ -87,16 +91,17 @@ struct Split {
         p.n = s.n;
         p.kt = key_tiles(s);
         p.ct = ceil_div(s.len, KT);
-        const int rts = row_tiles(a, s);
-        const int seg = n < (int64_t(1) << 31) ? int(uint32_t(pos - first) / uint32_t(p.kt))
-                                               : int((pos - first) / p.kt);
-        p.s0 = first + int64_t(seg) * p.kt;
-        p.hk = seg / rts;
-        p.rt = seg % rts;
+        const int rts = row_tiles(a, s), places = p.kt + kExtra;
+        const int seg = n < (int64_t(1) << 31) ? int(uint32_t(pos - first) / uint32_t(places))
+                                               : int((pos - first) / places);
+        p.s0 = first + int64_t(seg) * places;
         p.t0 = int(pos - p.s0);
         p.t1 = int(min64(p.kt, end - p.s0));
+        pos = min64(end, p.s0 + places);
+        if (p.t0 >= p.kt) continue;  // only the places behind the tiles
+        p.hk = seg / rts;
+        p.rt = seg % rts;
         p.rows = min(MR, s.n * a.G - p.rt * MR);
-        pos = p.s0 + p.t1;
         return true;
       }
       return false;
@@ -106,11 +111,12 @@ struct Split {
     // in it and goes on.
     __device__ int64_t slot(const Piece& p) const { return 2 * int64_t(blockIdx.x) + (p.t0 == 0); }
     // By the CTA in whose run the segment begins: the first and last CTA that
-    // hold a piece of it.
+    // hold a piece of it (place x is CTA ((x + 1) ctas - 1) / total's).
     __device__ void note(const Piece& p) const {
       const int rts = ceil_div(a.N * a.G, MR);
       a.seg[(int64_t(p.b) * a.Hkv + p.hk) * rts + p.rt] =
-          make_int2(int(blockIdx.x), p.whole() ? int(blockIdx.x) : int((p.s0 + p.kt - 1) / run));
+          make_int2(int(blockIdx.x), p.whole() ? int(blockIdx.x)
+                                               : int(((p.s0 + p.kt) * ctas - 1) / total));
     }
   };
 
@@ -122,7 +128,7 @@ struct Split {
     bool bad = false;
     int64_t total = 0, first = 0, base = 0;
     int b0 = a.B;
-    Pieces q{a, table, 0, 0, 1, 0, 0, 0};
+    Pieces q{a, table, 0, 0, 1, 0, 0, 0, 0};
     auto scan = [&](int64_t v) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -140,13 +146,11 @@ struct Split {
       total += __shfl_sync(0xffffffffu, in, 31);
     }
     if (bad && blockIdx.x == 0) atomicExch(a.err, kTreeBadInput);
-    q.run = total > 0 ? (total + gridDim.x - 1) / gridDim.x : 1;
-    q.pos = blockIdx.x * q.run;
-    q.end = min64(total, q.pos + q.run);
-    if (q.pos >= q.end) {
-      q.end = q.pos;
-      return q;
-    }
+    q.total = total;
+    q.ctas = int(min64(total, gridDim.x));
+    if (int(blockIdx.x) >= q.ctas) return q;  // an empty run
+    q.pos = total * blockIdx.x / q.ctas;
+    q.end = total * (blockIdx.x + 1) / q.ctas;
     for (int c = 0; c < a.B; c += 32) {
       if (a.B > 32) {  // (else the lane's values are those of the loop above)
         s = c + lane < a.B ? seq_dims(a, c + lane) : SeqDims{0, 0};
@@ -175,25 +179,48 @@ struct Split {
 };
 
 // Ancestor masks of the sequence's nodes, bit j of mask i: node j is on the
-// path from node i to the root, i included.  Doubling: mask(i) |= mask(up(i)),
-// up(i) = up(up(i)); ceil(log2 n) rounds for a chain of n.  By the
-// `threads` threads that call it (>= kMaxNodes / 2; thread tid of them), with
-// `sync` their barrier.  A parent outside [-1, i) counts as -1 and is reported.
+// path from node i to the root, i included.  Every thread walks its nodes' paths
+// up to kWalk steps; what is left of deeper trees goes by doubling, mask(i) |=
+// mask(up(i)), up(i) = up(up(i)).  By the `threads` threads that call it (>=
+// kMaxNodes / 2; thread tid of them), with `sync` their barrier; flag is a word
+// of shared memory.  A parent outside [-1, i) counts as -1 and is reported.
+constexpr int kWalk = 16;
 template <typename Sync>
 __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32_t* mask, int* up,
-                                            int* err, int tid, int threads, Sync sync) {
+                                            uint32_t* flag, int* err, int tid, int threads,
+                                            Sync sync) {
   for (int i = tid; i < n; i += threads) {
-    int p = parent ? parent[i] : i - 1;
+    int p = parent[i];
     if (p < -1 || p >= i) {
       atomicExch(err, kTreeBadInput);
       p = -1;
     }
     up[i] = p;
+  }
+  if (tid == 0) *flag = 0;
+  sync();
+  int left[2] = {-1, -1};
+  for (int k = 0, i = tid; i < n; ++k, i += threads) {
+    uint64_t m[4] = {0, 0, 0, 0};
+    int p = i;
+#pragma unroll 1
+    for (int step = 0; step <= kWalk && p >= 0; ++step) {
 #pragma unroll
-    for (int w = 0; w < kMaskWords; ++w) mask[i * kMaskWords + w] = (i >> 5) == w ? 1u << (i & 31) : 0;
+      for (int q = 0; q < 4; ++q)
+        if ((p >> 6) == q) m[q] |= uint64_t(1) << (p & 63);
+      p = up[p];
+    }
+    if (p >= 0) *flag = 1;
+    left[k] = p;
+    uint4* dst = reinterpret_cast<uint4*>(mask + i * kMaskWords);
+    dst[0] = make_uint4(uint32_t(m[0]), uint32_t(m[0] >> 32), uint32_t(m[1]), uint32_t(m[1] >> 32));
+    dst[1] = make_uint4(uint32_t(m[2]), uint32_t(m[2] >> 32), uint32_t(m[3]), uint32_t(m[3] >> 32));
   }
   sync();
-  for (int reach = 1; reach < n; reach <<= 1) {
+  if (*flag == 0) return;
+  for (int k = 0, i = tid; i < n; ++k, i += threads) up[i] = left[k];
+  sync();
+  for (int reach = kWalk + 1; reach < n; reach <<= 1) {
     // reads of this round, then its writes
     uint32_t add[2][kMaskWords];
     int nu[2];
@@ -222,6 +249,16 @@ __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32
     }
     sync();
   }
+}
+// Which of the 64 nodes k0 .. k0 + 63 node i sees: by the masks, or, with no
+// tree given (a chain), those up to i.
+__device__ __forceinline__ uint64_t sees(bool chain, const uint32_t* mask, int i, int k0) {
+  if (chain) {
+    const int d = i - k0;
+    return d < 0 ? 0 : d >= 63 ? ~uint64_t(0) : (uint64_t(2) << d) - 1;
+  }
+  const uint32_t* w = mask + i * kMaskWords + (k0 >> 5);
+  return w[0] | (uint64_t(w[1]) << 32);
 }
 
 // Workspace: 2 slots per CTA, each MR x D fp32 outputs, then the rows' running

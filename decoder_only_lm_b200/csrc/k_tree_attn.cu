@@ -42,7 +42,7 @@ struct Smem {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a) {
+__global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_constant__ TreeAttnArgs a) {
   using S = Split<MR, KT>;
   constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP;
   constexpr int V4 = D / 4;              // float4 of a row
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
   const int tid = threadIdx.x;
   const int r = tid >> 3, kk = tid & 7;  // row of the tile, lane of the row
   asm volatile("griddepcontrol.launch_dependents;");
-  auto pieces = S::plan(a, sm.table);
+  auto pieces = S::plan(a, sm.table, threadIdx.x < 32);
   __syncthreads();
   int mask_of = -1;  // sequence whose masks are in shared memory
   const float scale = rsqrtf(float(D)) * kLog2e;

@@ -6,21 +6,24 @@
 // A step of decoding reads every cached key and value once and does little with
 // them: with R = N G query rows per key/value head it is R FLOP a byte, so up
 // to a few hundred rows the cache's bandwidth bounds it, and what matters is
-// enough loads in flight.  A warp holds 16 query rows in registers (queries,
-// running maximum and sum, output); WM warps cover the rows of a tile and WK
-// warps share its keys (few rows: all warps split the keys and merge their
-// results at the end of a piece; then no warp waits for another while it
-// streams).  Key and value tiles come by 16-byte asynchronous copies into a
-// ring of stages, with the 16-byte chunks of a row XOR-swizzled so that the
-// matrix loads of 8 rows touch all banks.
+// enough loads in flight and few instructions a tile.  One lane of an extra warp
+// brings the tiles by TMA into a ring of stages, ahead across the pieces of its
+// CTA's run; the other warps wait for a stage and hand it back on their own, with
+// no barrier of the block between them.  A warp holds 16 query rows in registers
+// (queries, running maximum and sum, output); WM warps cover the rows of a tile
+// and WK warps share its keys (few rows: all of them split the keys and merge
+// their results at a piece's end).  The tensor maps' swizzle lets the matrix
+// loads of 8 rows touch all banks.
 //
 // Scores and probabilities stay in registers: the accumulator layout of
 // S = Q K^T is the operand layout of P for O += P V.  P is rounded to bf16 for
 // that product (the tensor cores' operand type; the sums of p stay fp32), as
 // in the training attention.
 
+#include "tc_common.cuh"
 #include "tree_attn.cuh"
 
+using namespace tc;
 using namespace tree;
 
 namespace {
@@ -29,33 +32,20 @@ constexpr int KT = 64;  // keys of a tile
 
 template <int D, int WM, int WK>
 struct Cfg {
-  static constexpr int kThreads = 32 * WM * WK;
+  static constexpr int NW = WM * WK;          // warps that compute
+  static constexpr int kThreads = 32 * (NW + 1);
   static constexpr int MR = 16 * WM;
   static constexpr int KW = KT / WK;          // keys of a warp
   static constexpr int kTile = KT * D * 2;    // bytes of a K (or V) tile
-  static constexpr int kStages = D == 128 ? 3 : 4;
-  static constexpr int kRing = kStages * 2 * kTile;
+  static constexpr int NS = D == 128 ? 2 : 3; // stages of K + V
+  static constexpr int kRing = NS * 2 * kTile;
   static constexpr int LO = D + 4;            // row stride of the merge buffer
-  static constexpr int kMerge = WK > 1 ? WK * MR * (LO + 2) * 4 : 0;
-  static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kSmem = kBuf + kMaxNodes * (kMaskWords + 1) * 4 + 16 + kTable * 8;
-  static constexpr int kCtas = WM == 8 ? (D == 128 ? 1 : 2) : D == 128 ? 2 : 3;  // per SM
+  static constexpr int kMerge = (WK - 1) * MR * (LO + 2) * 4;
+  static constexpr int kMasks = kMaxNodes * (kMaskWords + 1) * 4;
+  static constexpr int kSmem = 1024 + kRing + kMerge + kMasks + 512 + kListed * int(sizeof(Listed));
+  static constexpr int kCtas = WM == 8 ? 1 : D == 128 ? 2 : 3;  // per SM
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 bytes, or zeros where `real` is false
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -85,152 +75,204 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-// Byte offset of 16-byte chunk c of row r in a tile of D bf16 a row: the chunk
-// index is XORed with row bits so that 8 consecutive rows at one chunk fall
-// into 8 different 16-byte bank groups.
+// Byte offset of 16-byte chunk c of row r in a tile as TMA leaves it: boxes of
+// up to 64 channels, the chunk index within a box's row XORed with row bits so
+// that 8 consecutive rows at one chunk fall into 8 different bank groups (the
+// 128-, 64- and 32-byte swizzles).
 template <int D>
 __device__ __forceinline__ uint32_t at(int r, int c) {
-  constexpr int C = D / 8;  // chunks of a row
+  constexpr int C = D < 64 ? D / 8 : 8;  // chunks of a box's row
   const int x = C >= 8 ? (r & 7) : C == 4 ? ((r >> 1) & 3) : ((r >> 2) & 1);
-  return uint32_t(r * C + (c ^ x)) * 16;
+  return uint32_t((c / C) * (KT * 128) + (r * C + ((c % C) ^ x)) * 16);
 }
+// Tile t of a piece is wholly cached: no key of it is masked.
+__device__ __forceinline__ bool plain(const Piece& p, int t) { return (t + 1) * KT <= p.len; }
 
 template <int D, int WM, int WK>
 __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCtas)
-    tree_attn_mma_kernel(TreeAttnArgs a) {
+    tree_attn_mma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                         const __grid_constant__ CUtensorMap mx, const __grid_constant__ TreeAttnArgs a) {
   using F = Cfg<D, WM, WK>;
   using S = Split<F::MR, KT>;
-  constexpr int MR = F::MR, KW = F::KW, ST = F::kStages;
+  constexpr int MR = F::MR, KW = F::KW, NS = F::NS, NW = F::NW;
   constexpr int NT = KW / 8;   // score tiles of 8 keys
   constexpr int DT = D / 8;    // output tiles of 8 channels
   constexpr int KS = D / 16;   // steps of the score product
   constexpr int C = D / 8;     // 16-byte chunks of a row
-  // with all warps splitting the keys each streams its own rows of the tiles
-  constexpr bool kOwn = WM == 1;
-  extern __shared__ uint4 smem_raw[];
-  char* buf = reinterpret_cast<char*>(smem_raw);
-  const uint32_t ring = smem_addr(buf);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(buf + F::kBuf);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sring = smem_u32(ring);
+  float* ex = reinterpret_cast<float*>(ring + F::kRing);  // outputs, maxima and sums to merge
+  uint32_t* mask = reinterpret_cast<uint32_t*>(ring + F::kRing + F::kMerge);
   int* up = reinterpret_cast<int*>(mask + kMaxNodes * kMaskWords);
-  uint32_t* odd = reinterpret_cast<uint32_t*>(up + kMaxNodes);  // 64 bits: keys of non-finite V
-  SeqDims* table = reinterpret_cast<SeqDims*>(odd + 4);
+  // full[NS] | empty[NS] | listed[kListed] | rows
+  uint64_t* bars = reinterpret_cast<uint64_t*>(up + kMaxNodes);
+  const uint32_t b_rows = smem_u32(bars + 2 * NS + kListed);
+  Listed* list = reinterpret_cast<Listed*>(bars + 2 * NS + kListed + 1);
+  // nodes of non-finite values, 64 bits per node tile
+  uint64_t* bad = reinterpret_cast<uint64_t*>(list + kListed);
+  uint32_t* flag = reinterpret_cast<uint32_t*>(bad + kMaxNodes / 64);
+  SeqDims* table = reinterpret_cast<SeqDims*>(flag + 2);
+  auto b_full = [&](int s) { return smem_u32(bars + s); };
+  auto b_empty = [&](int s) { return smem_u32(bars + NS + s); };
+  auto b_listed = [&](int k) { return smem_u32(bars + 2 * NS + k % kListed); };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(b_full(s), 1);
+      mbar_init(b_empty(s), NW);
+    }
+    for (int k = 0; k < kListed; ++k) mbar_init(b_listed(k), 1);
+    mbar_init(b_rows, 32 * NW);
+    fence_mbar_init();
+    fence_proxy_async();
+  }
+  __syncthreads();
+
+  if (warp == NW) {
+    // ------------------------------------------------ loads
+    auto pieces = S::plan(a, table, true);
+    __syncwarp();
+    if (lane) return;
+    int g = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Listed& p = list[k % kListed];
+      Piece q;
+      if (pieces.next(q)) {
+        p.slot = pieces.slot(q);
+        if (q.t0 == 0) pieces.note(q);
+      } else {
+        q.kt = 0;
+      }
+      static_cast<Piece&>(p) = q;
+      mbar_arrive(b_listed(k));
+      if (q.kt == 0) break;
+      const int row0 = (q.b * a.Hkv + q.hk) * a.Tc;  // rows of the caches fit 31 bits
+      for (int t = q.t0; t < q.t1; ++t, ++g) {
+        const int s = g % NS;
+        if (!mbar_wait(b_empty(s), ((g / NS) & 1) ^ 1, a.err, 31)) {
+          ok = false;
+          break;
+        }
+        const bool fresh = t >= q.ct;
+        const uint32_t dk = sring + s * 2 * F::kTile, dv = dk + F::kTile;
+        const int y = fresh ? q.b * a.N + (t - q.ct) * KT : row0 + t * KT;
+        const int xk = fresh ? (a.H + q.hk) * D : 0, xv = fresh ? xk + a.Hkv * D : 0;
+        mbar_expect_tx(b_full(s), 2 * F::kTile);
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {
+          tma_load_2d(dk + c * KT * 2, fresh ? &mx : &mk, b_full(s), xk + c, y);
+          tma_load_2d(dv + c * KT * 2, fresh ? &mx : &mv, b_full(s), xv + c, y);
+        }
+      }
+    }
+    // every issued copy has landed before the CTA may exit
+    for (int q = max(0, g - NS); q < g; ++q) mbar_wait(b_full(q % NS), (q / NS) & 1, a.err, 32);
+    return;
+  }
+
+  // -------------------------------------------------- rows
   const int wm = warp % WM, wk = warp / WM;
   const int gr = lane >> 2, gc = lane & 3;  // fragment row and column pair
-  asm volatile("griddepcontrol.launch_dependents;");
-  auto pieces = S::plan(a, table);
-  __syncthreads();
-  int mask_of = -1;
+  int mask_of = -1, g = 0;
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+    const bool w = mbar_wait(bar, parity, a.err, where);
+    if (!__all_sync(0xffffffffu, w)) ok = false;
+  };
+  // barrier of these warps with a bounded wait: a warp that gave up does not
+  // leave the others waiting
+  uint32_t syncs = 0;
+  auto sync = [&] {
+    mbar_arrive(b_rows);
+    wait(b_rows, syncs++ & 1, 35);
+  };
   const float scale = rsqrtf(float(D)) * kLog2e;
   const bf16* qkv = static_cast<const bf16*>(a.qkv);
 
-  Piece pc;
-  while (pieces.next(pc)) {
-    const SeqDims s{pc.len, pc.n};
-    const int b = pc.b, hk = pc.hk, rt = pc.rt, t0 = pc.t0, t1 = pc.t1, ct = pc.ct, rows = pc.rows;
-    if (tid == 0 && t0 == 0) pieces.note(pc);
-    const bf16* xb = qkv + int64_t(b) * a.N * a.ld_qkv;
-    const bf16* kc = static_cast<const bf16*>(a.k) + (int64_t(b) * a.Hkv + hk) * a.Tc * D;
-    const bf16* vc = static_cast<const bf16*>(a.v) + (int64_t(b) * a.Hkv + hk) * a.Tc * D;
-    const bf16* kn = xb + int64_t(a.H + hk) * D;
-    const bf16* vn = kn + int64_t(a.Hkv) * D;
-    __syncthreads();  // the previous piece is done with shared memory
-
-    // one stage: the keys and values of tile t (zeros behind the last one)
-    auto load = [&](int t) {
-      if (t < t1) {
-        const bool fresh = t >= ct;
-        const int k0 = (fresh ? t - ct : t) * KT;
-        const int nk = (fresh ? s.n : s.len) - k0;
-        const bf16* kp = fresh ? kn + k0 * a.ld_qkv : kc + int64_t(k0) * D;
-        const bf16* vp = fresh ? vn + k0 * a.ld_qkv : vc + int64_t(k0) * D;
-        const int64_t ld = fresh ? a.ld_qkv : D;
-        const uint32_t dk = ring + uint32_t((t - t0) % ST) * (2 * F::kTile), dv = dk + F::kTile;
-        constexpr int kRows = kOwn ? KW : KT, kBy = kOwn ? 32 : F::kThreads;
-        const int r0 = kOwn ? wk * KW : 0, me = kOwn ? lane : tid;
-#pragma unroll
-        for (int e0 = 0; e0 < kRows * C; e0 += kBy) {
-          const int e = e0 + me;
-          if (kRows * C % kBy == 0 || e < kRows * C) {
-            const int r = r0 + e / C, c = e % C;
-            const bool real = r < nk;
-            const int64_t off = real ? r * ld + c * 8 : 0;
-            copy16(dk + at<D>(r, c), kp + off, real);
-            copy16(dv + at<D>(r, c), vp + off, real);
-          }
-        }
-      }
-      copy_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) load(t0 + i);
-
+  for (int k = 0;; ++k) {
+    wait(b_listed(k), (k / kListed) & 1, 34);
+    if (!ok) break;
+    const Listed& p = list[k % kListed];
+    if (p.kt == 0) break;
+    const bf16* xb = qkv + int64_t(p.b) * a.N * a.ld_qkv;
     // this warp's 16 query rows as matrix operands; zeros behind the last row
     uint32_t q[KS][4];
     int node[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = wm * 16 + gr + 8 * h;
-      const bool real = r < rows;
-      const int g = rt * MR + (real ? r : 0);
-      node[h] = g / a.G;
-      const bf16* p = xb + int64_t(node[h]) * a.ld_qkv + int64_t(hk * a.G + g % a.G) * D + 2 * gc;
+      const bool real = r < p.rows;
+      const int gq = p.rt * MR + (real ? r : 0);
+      node[h] = gq / a.G;
+      const bf16* src = xb + int64_t(node[h]) * a.ld_qkv + int64_t(p.hk * a.G + gq % a.G) * D + 2 * gc;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        q[k][h] = real ? *reinterpret_cast<const uint32_t*>(p + 16 * k) : 0u;
-        q[k][2 + h] = real ? *reinterpret_cast<const uint32_t*>(p + 16 * k + 8) : 0u;
+        q[k][h] = real ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+        q[k][2 + h] = real ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
       }
     }
-    if (a.parent && t1 > ct && mask_of != b) {
-      build_masks(a.parent + int64_t(b) * a.N, s.n, mask, up, odd + 2, a.err, tid, F::kThreads,
-                  [] { __syncthreads(); });
-      mask_of = b;
+    if (a.parent && p.t1 > p.ct && mask_of != p.b) {
+      sync();  // the last piece's masks are read no more
+      build_masks(a.parent + int64_t(p.b) * a.N, p.n, mask, up, flag, a.err, tid, 32 * NW, sync);
+      mask_of = p.b;
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[DT][4];
 #pragma unroll
     for (int j = 0; j < DT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    const bool busy = wm * 16 < rows;  // some row of this warp is real
+    const bool busy = wm * 16 < p.rows;  // some row of this warp is real
+    bool any_bad = false;
 
-    for (int t = t0; t < t1; ++t) {
-      const bool fresh = t >= ct;
-      copy_wait<ST - 2>();
-      // the tile has landed for every thread that reads it, and the stage
-      // loaded next has been read by all
-      if (kOwn && !fresh)
-        __syncwarp();
-      else
-        __syncthreads();
-      load(t + ST - 1);
-      const int k0 = (fresh ? t - ct : t) * KT;
-      const int nk = (fresh ? s.n : s.len) - k0 - wk * KW;  // keys of this warp
-      const uint32_t sk = ring + uint32_t((t - t0) % ST) * (2 * F::kTile), sv = sk + F::kTile;
-      uint64_t bad_v = 0;
-      if (fresh) {
-        // A node that a row may not see can hold anything, and 0 times a
-        // non-finite value is not 0: such value rows become 0 for the product
-        // and reach the rows that see them one by one below.
-        if (tid < 2) odd[tid] = 0;
-        __syncthreads();
-        char* vt = buf + (sv - ring);
-        for (int e = tid; e < KT * C; e += F::kThreads) {
-          const uint4 u = *reinterpret_cast<const uint4*>(vt + at<D>(e / C, e % C));
-          auto inf = [](uint32_t w) {
-            return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-          };
-          if (inf(u.x) || inf(u.y) || inf(u.z) || inf(u.w))
-            atomicOr(&odd[(e / C) >> 5], 1u << ((e / C) & 31));
+    for (int t = p.t0; t < p.t1; ++t, ++g) {
+      const int s = g % NS;
+      wait(b_full(s), (g / NS) & 1, 33);
+      if (!ok) break;
+      const bool fresh = t >= p.ct;
+      const int k0 = (fresh ? t - p.ct : t) * KT;
+      const int nk = (fresh ? p.n : p.len) - k0;  // keys of the tile
+      const int nw = nk - wk * KW;                // ... from this warp's first on
+      const uint32_t sk = sring + s * 2 * F::kTile, sv = sk + F::kTile;
+      if (!plain(p, t)) {
+        // Value rows behind the last key are foreign, and a node that a row may not
+        // see can hold anything: what is not this sequence's, and node values that
+        // are not finite (see add_nonfinite), become 0 for the product.
+        uint8_t* vt = ring + (sv - sring);
+        uint64_t drop = nk >= KT ? 0 : ~uint64_t(0) << nk;
+        if (fresh) {
+          uint64_t* word = bad + (k0 >> 6);
+          if (t == max(p.t0, p.ct)) {  // the piece's first: no other tile's words count
+            sync();                    // (the last piece's have been read)
+            if (tid < kMaxNodes / 64) bad[tid] = 0;
+            sync();
+          }
+          for (int e = tid; e < KT * C; e += 32 * NW) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vt + at<D>(e / C, e % C));
+            auto inf = [](uint32_t w) {
+              return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+            };
+            if (e / C < nk && (inf(u.x) || inf(u.y) || inf(u.z) || inf(u.w)))
+              atomicOr(reinterpret_cast<unsigned long long*>(word), 1ull << (e / C));
+          }
+          sync();
+          if (*word) {
+            any_bad = true;
+            drop |= *word;
+          }
         }
-        __syncthreads();
-        bad_v = odd[0] | (uint64_t(odd[1]) << 32);
-        if (bad_v) {
-          for (int e = tid; e < KT * C; e += F::kThreads)
-            if ((bad_v >> (e / C)) & 1)
+        if (drop) {
+          for (int e = tid; e < KT * C; e += 32 * NW)
+            if ((drop >> (e / C)) & 1)
               *reinterpret_cast<uint4*>(vt + at<D>(e / C, e % C)) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();  // before the stage is handed back
+          sync();
         }
-        __syncthreads();
+        if (!ok) break;
       }
-      if (!busy || nk <= 0) continue;
+      if (busy && nw > 0) {
       // scores
       float sc[NT][4];
 #pragma unroll
@@ -256,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
           mma16816(sc[j + 1], q[0], kb[2], kb[3]);
         }
       }
-      if (fresh || nk < KW) {
+      if (fresh || nw < KW) {
         uint64_t see[2] = {~uint64_t(0), ~uint64_t(0)};
         if (fresh) {
           see[0] = sees(!a.parent, mask, node[0], k0) >> (wk * KW);
@@ -267,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = j * 8 + gc * 2 + (e & 1);
-            if (key >= nk || !((see[e >> 1] >> key) & 1)) sc[j][e] = -INFINITY;
+            if (key >= nw || !((see[e >> 1] >> key) & 1)) sc[j][e] = -INFINITY;
           }
       }
       // running maximum (log2 domain: s scale), probabilities, sums
@@ -304,7 +346,7 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
       // O += P V
 #pragma unroll
       for (int k = 0; k < NT / 2; ++k) {
-        uint32_t p[4] = {pack2(sc[2 * k][0], sc[2 * k][1]), pack2(sc[2 * k][2], sc[2 * k][3]),
+        uint32_t pr[4] = {pack2(sc[2 * k][0], sc[2 * k][1]), pack2(sc[2 * k][2], sc[2 * k][3]),
                          pack2(sc[2 * k + 1][0], sc[2 * k + 1][1]),
                          pack2(sc[2 * k + 1][2], sc[2 * k + 1][3])};
         const int r = wk * KW + k * 16 + (lane & 15);
@@ -312,61 +354,87 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         for (int j = 0; j < DT; j += 2) {
           uint32_t vb[4];
           ldm4_trans(vb, sv + at<D>(r, j + (lane >> 4)));
-          mma16816(o[j], p, vb[0], vb[1]);
-          mma16816(o[j + 1], p, vb[2], vb[3]);
+          mma16816(o[j], pr, vb[0], vb[1]);
+          mma16816(o[j + 1], pr, vb[2], vb[3]);
         }
       }
-      if (bad_v) {
-        for (int key = 0; key < KW; ++key) {
-          if (!((bad_v >> (wk * KW + key)) & 1)) continue;
-          float p0 = 0.f, p1 = 0.f;  // from the lane of the row that holds this key
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (j * 8 + e == (key & ~7) + (key & 1)) {
-                p0 = sc[j][e];
-                p1 = sc[j][2 + e];
-              }
-          const int src = (lane & ~3) | ((key & 7) >> 1);
-          p0 = __shfl_sync(0xffffffffu, p0, src);
-          p1 = __shfl_sync(0xffffffffu, p1, src);
-          const bf16* v = vn + (k0 + wk * KW + key) * a.ld_qkv;
-#pragma unroll
-          for (int j = 0; j < DT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float ve = __bfloat162float(v[j * 8 + gc * 2 + e]);
-              if (p0 != 0.f) o[j][e] = fmaf(p0, ve, o[j][e]);
-              if (p1 != 0.f) o[j][2 + e] = fmaf(p1, ve, o[j][2 + e]);
-            }
-        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_empty(s));
     }
-    copy_wait<0>();
+    if (!ok) break;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       m[h] = __fmul_rn(m[h], scale);  // log2 domain, the base of the sums
     }
-    const bool whole = pc.whole();
-    float* w = a.ws + pieces.slot(pc) * slot_floats<MR>(D);
-    bf16* out = static_cast<bf16*>(a.out) + int64_t(b) * a.N * a.ld_out;
-    if (WK == 1) {
+    if constexpr (WK > 1) {
+      // the warps' results over the same rows, merged in warp order by the first
+      float* ml = ex + (WK - 1) * MR * F::LO;
+      if (wk > 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = (wk - 1) * MR + wm * 16 + gr + 8 * h;
+#pragma unroll
+          for (int j = 0; j < DT; ++j)
+            *reinterpret_cast<float2*>(ex + r * F::LO + 8 * j + 2 * gc) =
+                make_float2(o[j][2 * h], o[j][2 * h + 1]);
+          if (gc == 0) *reinterpret_cast<float2*>(ml + 2 * r) = make_float2(m[h], l[h]);
+        }
+      }
+      sync();
+      if (wk == 0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = wm * 16 + gr + 8 * h;
+          float2 u[WK - 1];
+          float M = m[h];
+#pragma unroll
+          for (int k = 0; k < WK - 1; ++k) {
+            u[k] = *reinterpret_cast<const float2*>(ml + 2 * (k * MR + r));
+            M = fmaxf(M, u[k].x);
+          }
+          const float f = m[h] == -INFINITY ? 0.f : ex2(m[h] - M);
+          l[h] *= f;
+#pragma unroll
+          for (int j = 0; j < DT; ++j) {
+            o[j][2 * h] *= f;
+            o[j][2 * h + 1] *= f;
+          }
+#pragma unroll
+          for (int k = 0; k < WK - 1; ++k) {
+            const float fk = u[k].x == -INFINITY ? 0.f : ex2(u[k].x - M);
+            l[h] = fmaf(fk, u[k].y, l[h]);
+#pragma unroll
+            for (int j = 0; j < DT; ++j) {
+              const float2 x =
+                  *reinterpret_cast<const float2*>(ex + (k * MR + r) * F::LO + 8 * j + 2 * gc);
+              o[j][2 * h] = fmaf(fk, x.x, o[j][2 * h]);
+              o[j][2 * h + 1] = fmaf(fk, x.y, o[j][2 * h + 1]);
+            }
+          }
+          m[h] = M;
+        }
+      }
+      sync();  // the buffer may take the next piece's results
+    }
+    if (wk == 0) {
+      bf16* out = static_cast<bf16*>(a.out) + int64_t(p.b) * a.N * a.ld_out;
+      float* w = a.ws + p.slot * slot_floats<MR>(D);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = wm * 16 + gr + 8 * h;
-        if (r >= rows) continue;
-        if (whole) {
-          const int hq = hk * a.G + (rt * MR + r) % a.G;
-          bf16* p = out + int64_t(node[h]) * a.ld_out + int64_t(hq) * D + 2 * gc;
+        if (r >= p.rows) continue;
+        if (p.whole()) {
+          const int hq = p.hk * a.G + (p.rt * MR + r) % a.G;
+          bf16* dst = out + int64_t(node[h]) * a.ld_out + int64_t(hq) * D + 2 * gc;
           const float inv = 1.f / l[h];
 #pragma unroll
           for (int j = 0; j < DT; ++j)
-            *reinterpret_cast<uint32_t*>(p + 8 * j) = pack2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
+            *reinterpret_cast<uint32_t*>(dst + 8 * j) = pack2(o[j][2 * h] * inv, o[j][2 * h + 1] * inv);
           if (a.lse && gc == 0)
-            a.lse[(int64_t(b) * a.H + hq) * a.N + node[h]] = (m[h] + log2f(l[h])) * kLn2;
+            a.lse[(int64_t(p.b) * a.H + hq) * a.N + node[h]] = (m[h] + log2f(l[h])) * kLn2;
         } else {
 #pragma unroll
           for (int j = 0; j < DT; ++j)
@@ -377,54 +445,16 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
             w[MR * D + MR + r] = l[h];
           }
         }
-      }
-    } else {
-      // the warps' results over the same rows, merged in warp order
-      float* ex = reinterpret_cast<float*>(buf);
-      float* ml = ex + WK * MR * F::LO;
-      __syncthreads();  // the last tile has been read
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = wk * MR + wm * 16 + gr + 8 * h;
-#pragma unroll
-        for (int j = 0; j < DT; ++j)
-          *reinterpret_cast<float2*>(ex + r * F::LO + 8 * j + 2 * gc) =
-              make_float2(o[j][2 * h], o[j][2 * h + 1]);
-        if (gc == 0) {
-          ml[2 * r] = m[h];
-          ml[2 * r + 1] = l[h];
-        }
-      }
-      __syncthreads();
-      for (int e = tid; e < rows * (D / 4); e += F::kThreads) {
-        const int r = e / (D / 4), c = e % (D / 4);
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int k = 0; k < WK; ++k) M = fmaxf(M, ml[2 * (k * MR + r)]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < WK; ++k) {
-          const float mk = ml[2 * (k * MR + r)];
-          const float f = mk == -INFINITY ? 0.f : ex2(mk - M);
-          const float4 x = *reinterpret_cast<const float4*>(ex + (k * MR + r) * F::LO + 4 * c);
-          L = fmaf(f, ml[2 * (k * MR + r) + 1], L);
-          acc.x = fmaf(f, x.x, acc.x);
-          acc.y = fmaf(f, x.y, acc.y);
-          acc.z = fmaf(f, x.z, acc.z);
-          acc.w = fmaf(f, x.w, acc.w);
-        }
-        if (whole) {
-          const int g = rt * MR + r, nd = g / a.G, hq = hk * a.G + g % a.G;
-          const float inv = 1.f / L;
-          *reinterpret_cast<uint2*>(out + int64_t(nd) * a.ld_out + int64_t(hq) * D + 4 * c) =
-              make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
-          if (a.lse && c == 0)
-            a.lse[(int64_t(b) * a.H + hq) * a.N + nd] = (M + log2f(L)) * kLn2;
-        } else {
-          *reinterpret_cast<float4*>(w + r * D + 4 * c) = acc;
-          if (c == 0) {
-            w[MR * D + r] = M;
-            w[MR * D + MR + r] = L;
+        if (any_bad) {
+          const int hq = p.hk * a.G + (p.rt * MR + r) % a.G;
+          for (int j = 0; j < DT; ++j) {
+            const int c = 8 * j + 2 * gc;
+            if (p.whole())
+              add_nonfinite<bf16, bf16>(a, p.b, p.hk, hq, node[h], p.n, bad, mask, m[h], 1.f / l[h],
+                                        out + int64_t(node[h]) * a.ld_out + int64_t(hq) * D, c, c + 2);
+            else
+              add_nonfinite<bf16, float>(a, p.b, p.hk, hq, node[h], p.n, bad, mask, m[h], 1.f,
+                                         w + r * D, c, c + 2);
           }
         }
       }
@@ -437,10 +467,18 @@ struct Variant {
   using F = Cfg<D, WM, WK>;
   static int grid() { return F::kCtas * gpt2_internal::sm_count(); }
   static int launch(const TreeAttnArgs& a, cudaStream_t st) {
+    CUtensorMap mk, mv, mx;
+    const int64_t rows = int64_t(a.B) * a.Hkv * a.Tc;
+    constexpr int box = D < 64 ? D : 64;
+    if (!make_map_rows(&mk, a.k, D, rows, D, box, KT) || !make_map_rows(&mv, a.v, D, rows, D, box, KT) ||
+        !make_map_rows(&mx, a.qkv, int64_t(a.H + 2 * a.Hkv) * D, int64_t(a.B) * a.N, a.ld_qkv, box, KT)) {
+      gpt2_internal::set_error("tree_attention: tensor map encoding failed");
+      return GPT2_ERR_CUDA;
+    }
     GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_mma_kernel<D, WM, WK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem));
     const TreeAttnArgs w = with_workspace<F::MR>(a, grid());
-    tree_attn_mma_kernel<D, WM, WK><<<grid(), F::kThreads, F::kSmem, st>>>(w);
+    tree_attn_mma_kernel<D, WM, WK><<<grid(), F::kThreads, F::kSmem, st>>>(mk, mv, mx, w);
     COUNT_LAUNCH(1);
     GPT2_LAUNCH_CHECK();
     return launch_combine<bf16, F::MR, D>(w, st);

@@ -69,7 +69,7 @@ __device__ __forceinline__ bool plain(const Piece& p, int t) { return (t + 1) * 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                        const __grid_constant__ CUtensorMap mx, const TreeAttnArgs a) {
+                        const __grid_constant__ CUtensorMap mx, const __grid_constant__ TreeAttnArgs a) {
   using F = Cfg<D>;
   constexpr int NS = F::NS, KC = F::KC;
   extern __shared__ uint8_t smem_raw[];
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_proxy_async();
   }
   if (warp == 1) tmem_alloc(smem_u32(slot), kTmemCols);
-  auto pieces = Split<MR, KT>::plan(a, table);
+  auto pieces = Split<MR, KT>::plan(a, table, threadIdx.x < 32);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

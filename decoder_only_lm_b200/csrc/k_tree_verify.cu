@@ -414,7 +414,7 @@ struct Walk {
 };
 
 template <bool kDraft, bool kCuts>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(TreeVerifyArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_constant__ TreeVerifyArgs a, int slice) {
   constexpr int K = kDraft ? 2 : 1;
   extern __shared__ uint64_t dyn[];  // w[slice], x[slice] (draft), the rows' cuts
   __shared__ Shared sh;

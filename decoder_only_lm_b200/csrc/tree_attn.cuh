@@ -53,20 +53,20 @@ struct Piece {
   int len, n, rows;  // the sequence's lengths, real rows of the row tile
   int kt, ct;        // key tiles of the segment, of them cache tiles
   int64_t s0;        // the segment's first tile in the list
-  __device__ bool whole() const { return t0 == 0 && t1 == kt; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == kt; }
 };
 
 template <int MR, int KT>
 struct Split {
-  __device__ static int row_tiles(const TreeAttnArgs& a, SeqDims s) {
+  __device__ __forceinline__ static int row_tiles(const TreeAttnArgs& a, SeqDims s) {
     return ceil_div(s.n * a.G, MR);
   }
   // key tiles of each segment of the sequence (0 when it has no node)
-  __device__ static int key_tiles(SeqDims s) {
+  __device__ __forceinline__ static int key_tiles(SeqDims s) {
     return s.n ? ceil_div(s.len, KT) + ceil_div(s.n, KT) : 0;
   }
   // places in the list
-  __device__ static int64_t tiles(const TreeAttnArgs& a, SeqDims s) {
+  __device__ __forceinline__ static int64_t tiles(const TreeAttnArgs& a, SeqDims s) {
     return s.n ? int64_t(a.Hkv) * row_tiles(a, s) * (key_tiles(s) + kExtra) : 0;
   }
 
@@ -77,7 +77,8 @@ struct Split {
     int64_t pos, end, total, first;
     int ctas;  // CTAs with a run: never more than places, so that none is empty
     int b0, b;
-    __device__ bool next(Piece& p) {
+    // (false: the run is done, p holds nothing)
+    __device__ __forceinline__ bool next(Piece& p) {
       while (pos < end) {
         const SeqDims s = b - b0 < kTable ? table[b - b0] : seq_dims(a, b);
         const int64_t n = tiles(a, s);
@@ -109,22 +110,32 @@ struct Split {
     // Workspace slot of a piece that is not a whole segment: 2 per CTA, the first
     // for a segment that began before the run, the second for one that begins
     // in it and goes on.
-    __device__ int64_t slot(const Piece& p) const { return 2 * int64_t(blockIdx.x) + (p.t0 == 0); }
+    __device__ __forceinline__ int64_t slot(const Piece& p) const { return 2 * int64_t(blockIdx.x) + (p.t0 == 0); }
+    __device__ __forceinline__ int last_cta(int64_t x1) const {  // of place x1 - 1
+      return total <= (1 << 20) && ctas <= 2048
+                 ? int((uint32_t(x1) * uint32_t(ctas) - 1) / uint32_t(total))
+                 : int((x1 * ctas - 1) / total);
+    }
     // By the CTA in whose run the segment begins: the first and last CTA that
     // hold a piece of it (place x is CTA ((x + 1) ctas - 1) / total's).
-    __device__ void note(const Piece& p) const {
+    __device__ __forceinline__ void note(const Piece& p) const {
       const int rts = ceil_div(a.N * a.G, MR);
       a.seg[(int64_t(p.b) * a.Hkv + p.hk) * rts + p.rt] =
-          make_int2(int(blockIdx.x), p.whole() ? int(blockIdx.x)
-                                               : int(((p.s0 + p.kt) * ctas - 1) / total));
+          make_int2(int(blockIdx.x), p.whole() ? int(blockIdx.x) : last_cta(p.s0 + p.kt));
     }
   };
 
-  // This CTA's run; every warp on its own, the table filled by the caller's
-  // first warp (a block barrier must follow).
-  __device__ static Pieces plan(const TreeAttnArgs& a, SeqDims* table) {
+  // floor(total c / ctas), in 32 bits where they do (64-bit divisions take longer
+  // than the rest of the plan)
+  __device__ __forceinline__ static int64_t share(int64_t total, int c, int ctas) {
+    return total <= (1 << 20) && ctas <= 2048 ? int64_t(uint32_t(total) * uint32_t(c) / uint32_t(ctas))
+                                              : total * c / ctas;
+  }
+
+  // This CTA's run, found by a whole warp; with `fill` it also writes the table
+  // (a barrier with the table's readers must follow).
+  __device__ __forceinline__ static Pieces plan(const TreeAttnArgs& a, SeqDims* table, bool fill) {
     const int lane = threadIdx.x & 31;
-    const bool fill = threadIdx.x < 32;
     bool bad = false;
     int64_t total = 0, first = 0, base = 0;
     int b0 = a.B;
@@ -149,8 +160,8 @@ struct Split {
     q.total = total;
     q.ctas = int(min64(total, gridDim.x));
     if (int(blockIdx.x) >= q.ctas) return q;  // an empty run
-    q.pos = total * blockIdx.x / q.ctas;
-    q.end = total * (blockIdx.x + 1) / q.ctas;
+    q.pos = share(total, blockIdx.x, q.ctas);
+    q.end = share(total, blockIdx.x + 1, q.ctas);
     for (int c = 0; c < a.B; c += 32) {
       if (a.B > 32) {  // (else the lane's values are those of the loop above)
         s = c + lane < a.B ? seq_dims(a, c + lane) : SeqDims{0, 0};
@@ -178,6 +189,17 @@ struct Split {
   }
 };
 
+// A run's pieces as one lane finds them and the CTA's other roles read them: kept
+// in shared memory (their state would cost every thread's registers), published
+// one by one, an empty one (kt = 0) last.  The lane that publishes also fills the
+// ring of NS <= 6 tile stages, at least one tile a piece, and waits for a stage's
+// release before it fills it again: when it writes piece k + kListed, every
+// reader has left piece k.
+constexpr int kListed = 8;
+struct Listed : Piece {
+  int64_t slot;  // workspace slot of the piece's results
+};
+
 // Ancestor masks of the sequence's nodes, bit j of mask i: node j is on the
 // path from node i to the root, i included.  Every thread walks its nodes' paths
 // up to kWalk steps; what is left of deeper trees goes by doubling, mask(i) |=
@@ -199,8 +221,12 @@ __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32
   }
   if (tid == 0) *flag = 0;
   sync();
-  int left[2] = {-1, -1};
-  for (int k = 0, i = tid; i < n; ++k, i += threads) {
+  int left[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + k * threads;
+    left[k] = -1;
+    if (i >= n) continue;
     uint64_t m[4] = {0, 0, 0, 0};
     int p = i;
 #pragma unroll 1
@@ -218,7 +244,9 @@ __device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32
   }
   sync();
   if (*flag == 0) return;
-  for (int k = 0, i = tid; i < n; ++k, i += threads) up[i] = left[k];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (tid + k * threads < n) up[tid + k * threads] = left[k];
   sync();
   for (int reach = kWalk + 1; reach < n; reach <<= 1) {
     // reads of this round, then its writes
@@ -261,6 +289,34 @@ __device__ __forceinline__ uint64_t sees(bool chain, const uint32_t* mask, int i
   return w[0] | (uint64_t(w[1]) << 32);
 }
 
+// Node values that are not finite: the products take zeros in their place (0
+// times such a value is not 0, and most rows may not see the node); the rows that
+// see one get its share here, after their results were stored by this thread:
+// channels [c0, c1) of a row whose result has base m (log2 domain), times inv_l,
+// the probability once more from the query and the key.  bad: 64 bits per 64
+// nodes.
+template <typename T, typename Out>
+__device__ __noinline__ void add_nonfinite(const TreeAttnArgs& a, int b, int hk, int hq, int node,
+                                           int n, const uint64_t* bad, const uint32_t* mask, float m,
+                                           float inv_l, Out* dst, int c0, int c1) {
+  const T* x = static_cast<const T*>(a.qkv) + int64_t(b) * a.N * a.ld_qkv;
+  const T* q = x + int64_t(node) * a.ld_qkv + int64_t(hq) * a.D;
+  const float scale = rsqrtf(float(a.D)) * kLog2e;
+  for (int k0 = 0; k0 < n; k0 += 64) {
+    const uint64_t keys = bad[k0 >> 6] & sees(!a.parent, mask, node, k0);
+    for (int j = 0; j < 64; ++j) {
+      if (!((keys >> j) & 1)) continue;
+      const T* k = x + int64_t(k0 + j) * a.ld_qkv + int64_t(a.H + hk) * a.D;
+      const T* v = k + int64_t(a.Hkv) * a.D;
+      float s = 0.f;
+      for (int d = 0; d < a.D; ++d) s = fmaf(to_f32<T>(q[d]), to_f32<T>(k[d]), s);
+      const float p = exp2f(fmaf(s, scale, -m)) * inv_l;
+      if (p != 0.f)
+        for (int c = c0; c < c1; ++c) dst[c] = from_f32<Out>(fmaf(p, to_f32<T>(v[c]), to_f32<Out>(dst[c])));
+    }
+  }
+}
+
 // Workspace: 2 slots per CTA, each MR x D fp32 outputs, then the rows' running
 // maximum (log2 domain) and sum, MR of each; then the segments' first and last
 // CTA.
@@ -281,79 +337,77 @@ TreeAttnArgs with_workspace(TreeAttnArgs a, int grid) {
 
 // The pieces of a split segment merged in order,
 //   M = max m_c,  out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,
-// by WPR warps per query row (1 or 4).  D / 4 lanes cover a row with 16-byte
-// loads, so 128 / D pieces of a warp are in flight at once.
-template <typename T, int MR, int D, int WPR>
-__global__ void __launch_bounds__(128) tree_combine_kernel(TreeAttnArgs a) {
-  constexpr int RPB = 4 / WPR;   // rows of a block
-  constexpr int LP = D / 4;      // lanes of a piece's row
-  constexpr int GP = 32 / LP;    // pieces at once
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float4 sh_o[WPR > 1 ? 4 : 1][WPR > 1 ? LP : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// by D / 4 lanes per query row (16-byte loads); kWide: a row's pieces shared by
+// the groups of lanes of a whole block, whose results are merged once more.
+// One pass, the running maximum kept: every load of a row is in flight at once,
+// and latency is what a merge of few pieces costs.
+template <typename T, int MR, int D, bool kWide>
+__global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeAttnArgs a) {
+  constexpr int LP = D / 4;                // lanes of a row
+  constexpr int NG = 128 / LP;             // groups of a block
+  constexpr int kAhead = 8;                // pieces in flight
+  __shared__ float4 sh_o[kWide ? 128 : 1];
+  __shared__ float2 sh_ml[kWide ? NG : 1];
+  const int group = threadIdx.x / LP, lane = threadIdx.x % LP;
   const uint32_t R = uint32_t(a.N) * a.G;  // rows of a (sequence, key/value head)
-  const uint32_t row = blockIdx.x * RPB + (WPR > 1 ? 0 : warp);
-  if (row >= uint32_t(a.B) * a.Hkv * R) return;  // WPR > 1: whole block
+  const uint32_t row = kWide ? blockIdx.x : blockIdx.x * NG + group;
+  if (row >= uint32_t(a.B) * a.Hkv * R) return;  // kWide: whole block
   const int r = int(row % R), bh = int(row / R), b = bh / a.Hkv, hk = bh % a.Hkv;
+  const bool there = r < seq_dims(a, b).n * a.G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 seg = a.seg[int64_t(bh) * ceil_div(int(R), MR) + r / MR];
-  if (r >= seq_dims(a, b).n * a.G) return;
+  if (!there) return;
   const int np = seg.y - seg.x + 1;  // the first in its CTA's second slot
   if (np == 1) return;               // finished by its CTA
   const int64_t sf = slot_floats<MR>(D);
   const int rr = r % MR;
-  auto piece = [&](int i) { return a.ws + (2 * int64_t(seg.x + i) + (i == 0)) * sf; };
-  float M = -INFINITY;
-  for (int i = lane; i < np; i += 32) M = fmaxf(M, piece(i)[MR * D + rr]);
-  M = warp_max(M);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  const int sub = WPR > 1 ? warp : 0;
-#pragma unroll 4
-  for (int i = sub * GP + lane / LP; i < np; i += WPR * GP) {
-    const float* p = piece(i);
-    const float m = p[MR * D + rr];
-    const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-    const float4 x = *reinterpret_cast<const float4*>(p + int64_t(rr) * D + lane % LP * 4);
-    o.x = fmaf(w, x.x, o.x);
-    o.y = fmaf(w, x.y, o.y);
-    o.z = fmaf(w, x.z, o.z);
-    o.w = fmaf(w, x.w, o.w);
-  }
+  float M = -INFINITY, l = 0.f;
+  auto add = [&](float m1, float l1, float4 x) {
+    const float mn = fmaxf(M, m1);
+    const float f0 = M == -INFINITY ? 0.f : exp2f(M - mn), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - mn);
+    M = mn;
+    l = fmaf(l, f0, l1 * f1);
+    o.x = fmaf(o.x, f0, x.x * f1);
+    o.y = fmaf(o.y, f0, x.y * f1);
+    o.z = fmaf(o.z, f0, x.z * f1);
+    o.w = fmaf(o.w, f0, x.w * f1);
+  };
+  constexpr int step = kWide ? NG : 1;
+  for (int i = kWide ? group : 0; i < np; i += kAhead * step) {
+    float mi[kAhead], li[kAhead];
+    float4 x[kAhead];
 #pragma unroll
-  for (int x = LP; x < 32; x <<= 1) {
-    o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
-    o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
-    o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
-    o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
-  }
-  for (int i = lane; i < np; i += 32) {
-    const float* p = piece(i);
-    const float m = p[MR * D + rr];
-    l = fmaf(m == -INFINITY ? 0.f : exp2f(m - M), p[MR * D + MR + rr], l);
-  }
-  l = warp_sum(l);
-  if (WPR > 1) {
-    if (lane < LP) sh_o[warp][lane] = o;
-    __syncthreads();
-    if (warp || lane >= LP) return;
-    o = sh_o[0][lane];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      const float4 x = sh_o[w][lane];
-      o.x += x.x;
-      o.y += x.y;
-      o.z += x.z;
-      o.w += x.w;
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = i + j * step;
+      const float* p = a.ws + (2 * int64_t(seg.x + c) + (c == 0)) * sf;
+      mi[j] = c < np ? p[MR * D + rr] : -INFINITY;
+      li[j] = c < np ? p[MR * D + MR + rr] : 0.f;
+      if (c < np) x[j] = *reinterpret_cast<const float4*>(p + int64_t(rr) * D + lane * 4);
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i + j * step < np) add(mi[j], li[j], x[j]);
   }
-  if (lane >= LP) return;
+  if (kWide) {
+    sh_o[threadIdx.x] = o;
+    if (lane == 0) sh_ml[group] = make_float2(M, l);
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int g = 1; g < NG; ++g) add(sh_ml[g].x, sh_ml[g].y, sh_o[g * LP + lane]);
+  }
   const int i = r / a.G, h = hk * a.G + r % a.G;
   T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + i) * a.ld_out + int64_t(h) * D + lane * 4;
   const float inv = 1.f / l;
-  out[0] = from_f32<T>(o.x * inv);
-  out[1] = from_f32<T>(o.y * inv);
-  out[2] = from_f32<T>(o.z * inv);
-  out[3] = from_f32<T>(o.w * inv);
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
   if (a.lse && lane == 0) a.lse[(int64_t(b) * a.H + h) * a.N + i] = (M + log2f(l)) * kLn2;
 }
 
@@ -362,19 +416,20 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(TreeAttnArgs a) {
 template <typename T, int MR, int D>
 int launch_combine(const TreeAttnArgs& a, cudaStream_t st) {
   const int64_t rows = int64_t(a.B) * a.N * a.H;
-  // few rows: each has many pieces, four warps share them
+  // few rows: each has many pieces, a block shares them
   const bool wide = rows < 8 * int64_t(gpt2_internal::sm_count());
+  constexpr int NG = 128 / (D / 4);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(unsigned(wide ? rows : cdiv64(rows, 4)));
+  cfg.gridDim = dim3(unsigned(wide ? rows : cdiv64(rows, NG)));
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  GPT2_CUDA_TRY(wide ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, D, 4>, a)
-                     : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, D, 1>, a));
+  GPT2_CUDA_TRY(wide ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, D, true>, a)
+                     : cudaLaunchKernelEx(&cfg, tree_combine_kernel<T, MR, D, false>, a));
   COUNT_LAUNCH(1);
   return GPT2_OK;
 }

@@ -5,20 +5,24 @@
 // key/value tiles of 64 are streamed once for up to 128 rows (nodes x query
 // heads of a key/value head).
 //
-// CTAs of 192 threads, two per SM, each with its run of key tiles:
-//   warp 0, one lane  TMA loads of the tiles (cache, then nodes) into a ring of
-//                     stages, ahead across the run's pieces;
-//   warp 1            owns the TMEM allocation; one lane issues S = Q K^T
-//                     (TMEM, double buffered) and O += P V (P in TMEM);
-//   warps 2-5         thread = query row = TMEM lane: running maximum and sum,
-//                     P (bf16) written over its own scores, O rescaled when a
-//                     maximum grows by more than 2^8, results at a piece's end.
+// Two CTAs of 192 threads per SM, each with its run of key tiles:
+//   warp 0            plans the run; one lane publishes its pieces and brings the
+//                     tiles (cache, then nodes) by TMA into a ring of stages,
+//                     ahead across the pieces;
+//   warp 1            owns the TMEM allocation; one lane issues S = Q K^T and
+//                     O += P V (P in TMEM);
+//   warps 2-5         thread = TMEM lane: running maximum and sum of a query
+//                     row, P (bf16) written over its own scores, O rescaled
+//                     when a maximum grows by more than 2^8, results at a
+//                     piece's end.
+// S has two buffers, so that the next tile's scores are there when a softmax
+// ends.
 // What a tile holds behind the last key (or the last node) is not the
-// sequence's: its scores are masked, and warps 2-5 clear its value rows before
-// the product.  They also bring the query rows, the next piece's before they
-// write a piece's results.  Warps without a real row only pass the barriers.
-// 256 TMEM columns and about 100 KB of shared memory let two CTAs share an SM,
-// so that one's softmax overlaps the other's MMAs.
+// sequence's: its scores are masked, and the row threads clear its value rows
+// before the product.  They also bring the query rows, the next piece's before
+// they write a piece's results.  Warps without a real row only pass barriers.
+// With two CTAs' shared memory little is left for the L1 cache, so nothing in
+// the steps may live in local memory (a spilled register costs an L2 access).
 //
 // Every wait is bounded (2 s) and reports a timeout in the error word.
 
@@ -31,21 +35,21 @@ using namespace tree;
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int MR = 128;  // query rows of a tile = TMEM lanes
-constexpr int KT = 64;   // keys of a tile
+constexpr int MR = 128;      // query rows of a tile = TMEM lanes = row threads
+constexpr int KT = 64;       // keys of a tile
 constexpr int kTmemCols = 256;
 constexpr float kRescale = 8.f;  // lazy-rescale threshold, log2 units
 
 template <int D>
 struct Cfg {
   static constexpr int KC = D / 64;              // 64-channel chunks of a row
-  static constexpr int kChunkQ = MR * 128;       // 16 KB: 128 rows x 64 bf16
+  static constexpr int kChunkQ = MR * 128;   // 16 KB: 128 rows x 64 bf16
   static constexpr int kChunk = KT * 128;        // 8 KB: 64 rows x 64 bf16
   static constexpr int kQ = KC * kChunkQ;
   static constexpr int kTile = KC * kChunk;      // a K (or V) tile
   static constexpr int NS = D == 64 ? 5 : 2;     // stages of K + V
   static constexpr int kMasks = kMaxNodes * (kMaskWords + 1) * 4;
-  static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + 512 + 1024;
+  static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + 1152 + 1024;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -62,14 +66,40 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-
+__device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16]) {
+  float v[16];
+  tmem_ld16(taddr, v);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+}
+// 16 columns of this thread's TMEM lane from registers; complete after tmem_wait_st()
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
 // Tile t of a piece is wholly cached: no key of it is masked.
 __device__ __forceinline__ bool plain(const Piece& p, int t) { return (t + 1) * KT <= p.len; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                        const __grid_constant__ CUtensorMap mx, const __grid_constant__ TreeAttnArgs a) {
+                        const __grid_constant__ CUtensorMap mx,
+                        const __grid_constant__ TreeAttnArgs a) {
   using F = Cfg<D>;
   constexpr int NS = F::NS, KC = F::KC;
   extern __shared__ uint8_t smem_raw[];
@@ -80,149 +110,199 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t* mask = reinterpret_cast<uint32_t*>(ring + NS * 2 * F::kTile);
   int* up = reinterpret_cast<int*>(mask + kMaxNodes * kMaskWords);
   uint64_t* bars = reinterpret_cast<uint64_t*>(up + kMaxNodes);
-  // q_full | kv_full[NS] | kv_empty[NS] | s_full[2] | s_free[2] | p_full[2] | o_done[2] | rows
+  // q_full | kv_full[NS] | kv_empty[NS] | s_full[2] | p_full[2] | o_done[2] | rows | listed[kListed]
   const uint32_t b_q = smem_u32(bars);
   auto b_kvf = [&](int s) { return smem_u32(bars + 1 + s); };
   auto b_kve = [&](int s) { return smem_u32(bars + 1 + NS + s); };
   auto b_sf = [&](int i) { return smem_u32(bars + 1 + 2 * NS + i); };
-  auto b_sfr = [&](int i) { return smem_u32(bars + 3 + 2 * NS + i); };
-  auto b_pf = [&](int i) { return smem_u32(bars + 5 + 2 * NS + i); };
-  auto b_od = [&](int i) { return smem_u32(bars + 7 + 2 * NS + i); };
-  const uint32_t b_rows = smem_u32(bars + 9 + 2 * NS);
-  uint32_t* slot = reinterpret_cast<uint32_t*>(bars + 10 + 2 * NS);
-  SeqDims* table = reinterpret_cast<SeqDims*>(slot + 6);
-  uint32_t* odd = slot + 1;  // keys of a node tile whose values are not finite
+  auto b_pf = [&](int i) { return smem_u32(bars + 3 + 2 * NS + i); };
+  auto b_od = [&](int i) { return smem_u32(bars + 5 + 2 * NS + i); };
+  const uint32_t b_rows = smem_u32(bars + 7 + 2 * NS);
+  auto b_listed = [&](int k) { return smem_u32(bars + 8 + 2 * NS + k % kListed); };
+  Listed* list = reinterpret_cast<Listed*>(bars + 8 + 2 * NS + kListed);
+  uint64_t* bad = reinterpret_cast<uint64_t*>(list + kListed);  // nodes of non-finite values
+  uint32_t* flag = reinterpret_cast<uint32_t*>(bad + kMaxNodes / 64);
+  uint32_t* slot = flag + 1;
+  SeqDims* table = reinterpret_cast<SeqDims*>(flag + 2);
+  // tile g: buffer of its scores, and parity of the buffer's use
+  auto buf_of = [](int g) { return g & 1; };
+  auto par_of = [](int g) { return uint32_t((g >> 1) & 1); };
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(int(threadIdx.x / 32)), lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     mbar_init(b_q, 1);
-    mbar_init(b_rows, 128);
+    mbar_init(b_rows, MR);
     for (int s = 0; s < NS; ++s) {
       mbar_init(b_kvf(s), 1);
       mbar_init(b_kve(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sf(i), 1);
-      mbar_init(b_sfr(i), 128);
-      mbar_init(b_pf(i), 128);
+      mbar_init(b_pf(i), MR);
       mbar_init(b_od(i), 1);
     }
+    for (int k = 0; k < kListed; ++k) mbar_init(b_listed(k), 1);
     fence_mbar_init();
     fence_proxy_async();
   }
+  __syncwarp();
   if (warp == 1) tmem_alloc(smem_u32(slot), kTmemCols);
-  auto pieces = Split<MR, KT>::plan(a, table, threadIdx.x < 32);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const uint32_t tS = tmem, tO = tmem + 128;  // S buffers at +0 and +64, O at +128
+  // S buffers at +0 and +64, O at +128
+  const uint32_t tS = tmem, tO = tmem + 128;
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------ TMA
-    int g = 0;
-    bool ok = true;
-    Piece p;
-    while (ok && pieces.next(p)) {
-      const int row0 = (p.b * a.Hkv + p.hk) * a.Tc;  // B Hkv Tc rows of >= 128 B fit 31 bits
-      for (int t = p.t0; t < p.t1; ++t, ++g) {
-        const int s = g % NS;
-        if (!mbar_wait(b_kve(s), ((g / NS) & 1) ^ 1, a.err, 11)) {
-          ok = false;
-          break;
+  if (warp == 0) {
+    // ------------------------------------------------ plan, loads
+    auto pieces = Split<MR, KT>::plan(a, table, true);
+    __syncwarp();
+    if (lane == 0) {
+      int s = 0;          // stage, and how often the ring has come round
+      uint32_t round = 0;
+      int filled = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        Listed& p = list[k % kListed];
+        Piece q;
+        if (pieces.next(q)) {
+          p.slot = pieces.slot(q);
+          if (q.t0 == 0) pieces.note(q);
+        } else {
+          q.kt = 0;
         }
-        const bool fresh = t >= p.ct;
-        const uint32_t dk = sKV + s * 2 * F::kTile, dv = dk + F::kTile;
-        const int y = fresh ? p.b * a.N + (t - p.ct) * KT : row0 + t * KT;
-        const int xk = fresh ? (a.H + p.hk) * D : 0, xv = fresh ? xk + a.Hkv * D : 0;
-        mbar_expect_tx(b_kvf(s), 2 * F::kTile);
+        static_cast<Piece&>(p) = q;
+        mbar_arrive(b_listed(k));
+        if (q.kt == 0) break;
+        const int row0 = (q.b * a.Hkv + q.hk) * a.Tc;  // rows of the caches fit 31 bits
+        for (int t = q.t0; t < q.t1; ++t) {
+          if (!mbar_wait(b_kve(s), (round & 1) ^ 1, a.err, 11)) {
+            ok = false;
+            break;
+          }
+          const bool fresh = t >= q.ct;
+          const uint32_t dk = sKV + s * 2 * F::kTile, dv = dk + F::kTile;
+          const int y = fresh ? q.b * a.N + (t - q.ct) * KT : row0 + t * KT;
+          const int xk = fresh ? (a.H + q.hk) * D : 0, xv = fresh ? xk + a.Hkv * D : 0;
+          mbar_expect_tx(b_kvf(s), 2 * F::kTile);
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          tma_load_2d(dk + c * F::kChunk, fresh ? &mx : &mk, b_kvf(s), xk + 64 * c, y);
-          tma_load_2d(dv + c * F::kChunk, fresh ? &mx : &mv, b_kvf(s), xv + 64 * c, y);
+          for (int c = 0; c < KC; ++c) {
+            tma_load_2d(dk + c * F::kChunk, fresh ? &mx : &mk, b_kvf(s), xk + 64 * c, y);
+            tma_load_2d(dv + c * F::kChunk, fresh ? &mx : &mv, b_kvf(s), xv + 64 * c, y);
+          }
+          ++filled;
+          if (++s == NS) {
+            s = 0;
+            ++round;
+          }
         }
       }
+      // every issued copy has landed before the CTA may exit
+      for (int q = max(0, filled - NS); q < filled; ++q) mbar_wait(b_kvf(q % NS), (q / NS) & 1, a.err, 15);
     }
-    // every issued copy has landed before the CTA may exit
-    for (int q = max(0, g - NS); q < g; ++q) mbar_wait(b_kvf(q % NS), (q / NS) & 1, a.err, 15);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ------------------------------------------------ MMA
+    // The whole warp runs the loop, so that its control and the descriptors are
+    // warp-uniform (from one lane's branch every operand of an MMA has to be moved
+    // to the uniform registers first), and one elected lane issues.
+    const bool leader = elect_one();
     const uint32_t id_s = idesc_bf16(MR, KT, 0, 0), id_o = idesc_bf16(MR, D, 0, 1);
     const uint64_t dQ = desc_kmajor(sQ, 0), dK = desc_kmajor(sKV, 0);
     const uint64_t dV = desc_mnmajor(sKV + F::kTile, 0);
-    int g = 0, k = 0;
+    const uint32_t uS = uniform(tS), uO = uniform(tO);
+    int g = 0, s = 0, last = 0;  // tile, its stage, the stage of the tile before
+    uint32_t round = 0;
     bool ok = true;
-    auto issue_pv = [&](int gt, bool acc) -> bool {
-      if (!mbar_wait(b_pf(gt & 1), (gt >> 1) & 1, a.err, 13)) return false;
-      tc_fence_after();
-      const uint64_t v = desc_offset(dV, (gt % NS) * 2 * F::kTile);
-      const uint32_t pa = tS + (gt & 1) * KT;
-      if (acc)
-        umma_ts_i<1>(tO, pa, v, id_o);
-      else
-        umma_ts_i<0>(tO, pa, v, id_o);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) umma_ts_i<1>(tO, pa + 8 * i, v + i * 128, id_o);
-      umma_commit(b_od(gt & 1));
-      umma_commit(b_kve(gt % NS));
-      return true;
+    auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+      const bool w = mbar_wait(bar, parity, a.err, where);
+      if (!__all_sync(0xffffffffu, w)) ok = false;
     };
-    Piece p;
-    for (; ok && pieces.next(p); ++k) {
-      if (!mbar_wait(b_q, k & 1, a.err, 12)) break;
-      for (int t = p.t0; t < p.t1; ++t, ++g) {
-        const int s = g % NS;
-        if (!mbar_wait(b_kvf(s), (g / NS) & 1, a.err, 12) ||
-            !mbar_wait(b_sfr(g & 1), ((g >> 1) & 1) ^ 1, a.err, 12)) {
-          ok = false;
-          break;
-        }
+    // O += P V of tile gt in stage st
+    auto issue_pv = [&](int gt, int st, bool acc) {
+      wait(b_pf(buf_of(gt)), par_of(gt), 13);
+      if (!ok) return;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t v = desc_offset(dV, st * 2 * F::kTile);
+        const uint32_t pa = uS + buf_of(gt) * KT;
+        if (acc)
+          umma_ts_i<1>(uO, pa, v, id_o);
+        else
+          umma_ts_i<0>(uO, pa, v, id_o);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) umma_ts_i<1>(uO, pa + 8 * i, v + i * 128, id_o);
+        umma_commit(b_od(buf_of(gt)));
+        umma_commit(b_kve(st));
+      }
+      __syncwarp();
+    };
+    for (int k = 0; ok; ++k) {
+      wait(b_listed(k), (k / kListed) & 1, 25);
+      const int kt = uniform(list[k % kListed].kt), t0 = uniform(list[k % kListed].t0);
+      const int t1 = uniform(list[k % kListed].t1);
+      if (!ok || kt == 0) break;
+      wait(b_q, k & 1, 12);
+      for (int t = t0; ok && t < t1; ++t, ++g) {
+        // (the scores' buffer is free: it held the probabilities of tile g - 2,
+        // whose product was issued before this)
+        wait(b_kvf(s), round & 1, 12);
+        if (!ok) break;
         tc_fence_after();
-        const uint64_t kd = desc_offset(dK, s * 2 * F::kTile);
+        if (leader) {
+          const uint64_t kd = desc_offset(dK, s * 2 * F::kTile);
+          const uint32_t ts = uS + buf_of(g) * KT;
 #pragma unroll
-        for (int c = 0; c < KC; ++c)
+          for (int c = 0; c < KC; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint64_t qa = desc_offset(dQ, c * F::kChunkQ) + 2 * i;
-            const uint64_t kb = desc_offset(kd, c * F::kChunk) + 2 * i;
-            if (c == 0 && i == 0)
-              umma_i<0>(tS + (g & 1) * KT, qa, kb, id_s);
-            else
-              umma_i<1>(tS + (g & 1) * KT, qa, kb, id_s);
-          }
-        umma_commit(b_sf(g & 1));
-        if (t > p.t0 && !issue_pv(g - 1, t - 1 > p.t0)) {
-          ok = false;
-          break;
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t qa = desc_offset(dQ, c * F::kChunkQ) + 2 * i;
+              const uint64_t kb = desc_offset(kd, c * F::kChunk) + 2 * i;
+              if (c == 0 && i == 0)
+                umma_i<0>(ts, qa, kb, id_s);
+              else
+                umma_i<1>(ts, qa, kb, id_s);
+            }
+          umma_commit(b_sf(buf_of(g)));
+        }
+        __syncwarp();
+        if (t > t0) issue_pv(g - 1, last, t - 1 > t0);
+        last = s;
+        if (++s == NS) {
+          s = 0;
+          ++round;
         }
       }
-      if (ok) ok = issue_pv(g - 1, p.t1 - 1 > p.t0);
+      if (ok) issue_pv(g - 1, last, t1 - 1 > t0);
     }
     // all issued MMAs complete before TMEM is released
-    if (g > 0) mbar_wait(b_od((g - 1) & 1), ((g - 1) >> 1) & 1, a.err, 16);
-  } else if (warp >= 2) {
+    if (g > 0) mbar_wait(b_od(buf_of(g - 1)), par_of(g - 1), a.err, 16);
+  } else {
     // ------------------------------------------------ rows
-    const int e = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const int row = (warp & 3) * 32 + lane;  // of the tile; TMEM lane
     const uint32_t lo = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tOw = tO + lo;            // this lane's output
     const float scale = rsqrtf(float(D)) * kLog2e;
     const bf16* qkv = static_cast<const bf16*>(a.qkv);
     int g = 0, mask_of = -1;
     bool ok = true;
-    uint32_t syncs = 0;
-    // the 128 row threads, with a bounded wait (a warp that gave up does not
-    // leave the others waiting)
-    auto rows_sync = [&] {
-      mbar_arrive(b_rows);
-      const bool w = mbar_wait(b_rows, syncs++ & 1, a.err, 22);
+    auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+      const bool w = mbar_wait(bar, parity, a.err, where);
       if (!__all_sync(0xffffffffu, w)) ok = false;
     };
-    Piece p;
-    // the query rows of a piece (every MMA that read the last piece's is
-    // complete: its scores have been taken)
+    // barrier of the row threads with a bounded wait: a warp that gave up does
+    // not leave the others waiting
+    uint32_t syncs = 0;
+    auto rows_sync = [&] {
+      mbar_arrive(b_rows);
+      wait(b_rows, syncs++ & 1, 22);
+    };
+    // the query rows of a piece (every MMA that read the last piece's is complete:
+    // its scores have been taken)
     auto load_q = [&](const Piece& q) {
-      const bool real = e < q.rows;
-      const int gr = q.rt * MR + (real ? e : 0), node = gr / a.G, h = q.hk * a.G + gr % a.G;
+      const bool real = row < q.rows;
+      const int gr = q.rt * MR + (real ? row : 0), node = gr / a.G, h = q.hk * a.G + gr % a.G;
       const uint4* src = reinterpret_cast<const uint4*>(
           qkv + (int64_t(q.b) * a.N + node) * a.ld_qkv + int64_t(h) * D);
 #pragma unroll
@@ -232,208 +312,177 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int c = 0; c < 8; ++c) v[c] = real ? src[c0 + c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(smem + (c0 >> 3) * F::kChunkQ + e * 128 + ((c ^ (e & 7)) << 4)) = v[c];
+          *reinterpret_cast<uint4*>(smem + (c0 >> 3) * F::kChunkQ + row * 128 + ((c ^ (row & 7)) << 4)) = v[c];
       }
       fence_proxy_async();  // visible to the MMAs
       rows_sync();
-      if (e == 0) mbar_arrive(b_q);
+      if (row == 0) mbar_arrive(b_q);
     };
-    // A tile with foreign rows, or with nodes that a row may not see: those can
-    // hold anything, and 0 times a non-finite value is not 0.  Value rows behind
-    // the last key become 0; so do rows with non-finite values among the nodes,
-    // whose keys are returned (they reach the rows that see them one by one).
-    auto clear = [&](const Piece& q, int t, int gt) -> uint64_t {
+    // A tile with foreign rows, or with nodes that a row may not see: value rows
+    // behind the last key become 0, and so do node rows with non-finite values,
+    // which are noted in `bad` (see add_nonfinite).
+    auto clear = [&](const Piece& q, int t, int gt) -> bool {
       const int s = gt % NS;
       const bool fresh = t >= q.ct;
       const int nk = fresh ? q.n - (t - q.ct) * KT : q.len - t * KT;
-      const bool w = mbar_wait(b_kvf(s), (gt / NS) & 1, a.err, 21);  // complete: its scores are
-      if (!__all_sync(0xffffffffu, w)) ok = false;
+      wait(b_kvf(s), (gt / NS) & 1, 21);  // complete: its scores are
       uint8_t* v = ring + s * 2 * F::kTile + F::kTile;
       uint64_t drop = nk >= KT ? 0 : ~uint64_t(0) << nk;
-      uint64_t bad_v = 0;
+      bool found = false;
       if (fresh) {
-        if (e < 2) odd[e] = 0;
-        rows_sync();
-#pragma unroll
-        for (int x = e; x < KT * D / 8; x += 128) {  // 16-byte units, the swizzle left alone
+        uint64_t* word = bad + (t - q.ct);
+        if (t == max(q.t0, q.ct)) {  // the piece's first: no other tile's words count
+          rows_sync();               // (the last piece's have been read)
+          if (row < kMaxNodes / 64) bad[row] = 0;
+          rows_sync();
+        }
+        for (int x = row; x < KT * D / 8; x += MR) {  // 16-byte units, the swizzle left alone
           const int r = x / 8 % KT;
           const uint4 u = *reinterpret_cast<const uint4*>(v + x * 16);
           auto inf = [](uint32_t w2) {
             return (w2 & 0x7F80u) == 0x7F80u || (w2 & 0x7F800000u) == 0x7F800000u;
           };
           if (r < nk && (inf(u.x) || inf(u.y) || inf(u.z) || inf(u.w)))
-            atomicOr(&odd[r >> 5], 1u << (r & 31));
+            atomicOr(reinterpret_cast<unsigned long long*>(word), 1ull << r);
         }
         rows_sync();
-        bad_v = odd[0] | (uint64_t(odd[1]) << 32);
-        drop |= bad_v;
+        found = *word != 0;
+        drop |= *word;
       }
       if (drop) {
-        for (int x = e; x < KT * D / 8; x += 128)
+        for (int x = row; x < KT * D / 8; x += MR)
           if ((drop >> (x / 8 % KT)) & 1) *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async();  // before this thread's arrival that the product waits for
       }
-      return bad_v;
+      return found;
     };
-    bool have = pieces.next(p);
-    if (have) load_q(p);
-    while (ok && have) {
-      const bool real = e < p.rows;
-      const bool busy = ((warp & 3) * 32) < p.rows;
-      const int gr = p.rt * MR + (real ? e : 0), node = gr / a.G, hq = p.hk * a.G + gr % a.G;
-      if (e == 0 && p.t0 == 0) pieces.note(p);
-      if (a.parent && p.t1 > p.ct && mask_of != p.b) {
-        build_masks(a.parent + int64_t(p.b) * a.N, p.n, mask, up, odd + 2, a.err, e, 128, rows_sync);
+    wait(b_listed(0), 0, 26);
+    if (ok && list[0].kt > 0) load_q(list[0]);
+    for (int k = 0; ok; ++k) {
+      const Listed& p = list[k % kListed];
+      if (p.kt == 0) break;
+      const int rows = p.rows, t1 = p.t1, len = p.len, ct = p.ct, pn = p.n;
+      const bool real = row < rows;
+      const bool busy = (row & ~31) < rows;  // some row of this warp is real
+      const int gr = p.rt * MR + (real ? row : 0), node = gr / a.G;
+      if (a.parent && t1 > ct && mask_of != p.b) {
+        build_masks(a.parent + int64_t(p.b) * a.N, pn, mask, up, flag, a.err, row, MR, rows_sync);
         mask_of = p.b;
       }
+      bool any_bad = false, first = true;
       float m = -INFINITY, l = 0.f;
-      for (int t = p.t0; t < p.t1; ++t, ++g) {
-        bool wt = mbar_wait(b_sf(g & 1), (g >> 1) & 1, a.err, 14);
-        if (!__all_sync(0xffffffffu, wt)) {
-          ok = false;
-          break;
-        }
-        const uint64_t bad_v = plain(p, t) ? 0 : clear(p, t, g);
+      for (int t = p.t0; t < t1; ++t, ++g, first = false) {
+        wait(b_sf(buf_of(g)), par_of(g), 14);
+        if ((t + 1) * KT > len) any_bad |= clear(p, t, g);
         if (!ok) break;
         if (!busy) {
-          mbar_arrive(b_sfr(g & 1));
-          mbar_arrive(b_pf(g & 1));
+          mbar_arrive(b_pf(buf_of(g)));
           continue;
         }
         tc_fence_after();
-        uint32_t r0[32], r1[32];
-        tmem_ld32_async(tS + lo + (g & 1) * KT, r0);
-        tmem_ld32_async(tS + lo + (g & 1) * KT + 32, r1);
-        tmem_wait_ld(r0);
-        reg_after_wait(r1);
-        tc_fence_before();
-        mbar_arrive(b_sfr(g & 1));
-        float x[64];  // raw scores; keys that the row may not see become -inf
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = __uint_as_float(r0[i]);
-          x[32 + i] = __uint_as_float(r1[i]);
-        }
-        if (!plain(p, t)) {
-          const bool fresh = t >= p.ct;
-          const int k0 = (fresh ? t - p.ct : t) * KT, nk = (fresh ? p.n : p.len) - k0;
-          uint64_t see = nk >= KT ? ~uint64_t(0) : (uint64_t(1) << nk) - 1;
+        const uint32_t tSw = tS + lo + buf_of(g) * KT;
+        const bool open = (t + 1) * KT <= len;  // no key masked
+        uint64_t see = ~uint64_t(0);
+        if (!open) {
+          const bool fresh = t >= ct;
+          const int k0 = (fresh ? t - ct : t) * KT, nk = (fresh ? pn : len) - k0;
+          if (nk < KT) see = (uint64_t(1) << nk) - 1;
           if (fresh) see &= sees(!a.parent, mask, node, k0);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) x[i] = (see >> i) & 1 ? x[i] : -INFINITY;
         }
-        float c4[4];
+        // Two halves of 32 keys: x = raw scores, keys that the row may not see
+        // -inf.  The base m of the probabilities (log2 domain) follows the
+        // maximum only when it grows by more than 2^8 (they stay <= 256); 0 is
+        // used while the row has seen nothing (every p is then 2^(-inf) = 0).
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float* y = x + 16 * k;
-          float mm = max3f(y[0], y[1], y[2]);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tmem_ld32_async(tSw + 32 * h, r);
+          tmem_wait_ld(r);
+          float x[32];
 #pragma unroll
-          for (int i = 3; i < 15; i += 2) mm = max3f(mm, y[i], y[i + 1]);
-          c4[k] = fmaxf(mm, y[15]);
-        }
-        // log2 domain; the base of the probabilities follows the maximum only
-        // when it grows by more than 2^8 (they stay <= 256); 0 while the row
-        // has seen nothing (every p is then 2^(-inf) = 0)
-        const float mn = fmaxf(m, __fmul_rn(max3f(c4[0], c4[1], fmaxf(c4[2], c4[3])), scale));
-        const bool resc = mn > m + kRescale;
-        const float mu = resc ? mn : m;
-        const float corr = resc ? ex2(m - mn) : 1.f;
-        const float base = mu == -INFINITY ? 0.f : mu;
-        uint32_t pk[32];
-        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+          if (!open) {
+            const uint32_t bits = uint32_t(see >> (32 * h));
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float u0, u1;
-          fma2(u0, u1, x[i], x[i + 1], scale, scale, -base, -base);
-          const float p0 = ex2(u0), p1 = ex2(u1);
-          add2(sa[(i >> 1) & 3], sb[(i >> 1) & 3], p0, p1);
-          pk[i >> 1] = pack2(p0, p1);
-        }
-        const float rs = ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
-        l = l * corr + rs;
-        m = mu;
-        if (t > p.t0 && __any_sync(0xffffffffu, resc)) {
-          // O must hold the last tile's product before it is rescaled
-          wt = mbar_wait(b_od((g - 1) & 1), ((g - 1) >> 1) & 1, a.err, 17);
-          if (!__all_sync(0xffffffffu, wt)) {
-            ok = false;
-            break;
+            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1 ? x[i] : -INFINITY;
           }
-          tc_fence_after();
+          float c2[2];
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            float f[32];
-            tmem_ld32_async(tO + lo + c, o);
-            tmem_wait_ld(o);
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const float* y = x + 16 * k2;
+            float mm = max3f(y[0], y[1], y[2]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * corr;
-            tmem_st32(tO + lo + c, f);
+            for (int i = 3; i < 15; i += 2) mm = max3f(mm, y[i], y[i + 1]);
+            c2[k2] = fmaxf(mm, y[15]);
           }
+          const float mn = __fmul_rn(fmaxf(c2[0], c2[1]), scale);
+          const bool resc = mn > m + kRescale;
+          if (__any_sync(0xffffffffu, resc)) {
+            const float corr = resc ? ex2(m - mn) : 1.f;
+            if (resc) m = mn;
+            l *= corr;
+            if (h == 1) {  // the first half's probabilities had the old base
+              uint32_t q[16];
+              tmem_wait_st();
+              tmem_ld16_raw(tSw, q);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&q[i]);
+                q[i] = pack2(__low2float(v) * corr, __high2float(v) * corr);
+              }
+              tmem_st16_async(tSw, q);
+            }
+            if (!first) {  // O holds the last step's product
+              wait(b_od(buf_of(g - 1)), par_of(g - 1), 17);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16_raw(tOw + c, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                tmem_st16_async(tOw + c, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          uint32_t pk[16];
+          float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float u0, u1;
+            fma2(u0, u1, x[i], x[i + 1], scale, scale, -base, -base);
+            const float p0 = ex2(u0), p1 = ex2(u1);
+            add2(sa[(i >> 1) & 1], sb[(i >> 1) & 1], p0, p1);
+            pk[i >> 1] = pack2(p0, p1);
+          }
+          l += (sa[0] + sb[0]) + (sa[1] + sb[1]);
+          // P (bf16) over the first 32 columns of its scores, the A operand of
+          // P V: a half's 16 columns were read by the first load
+          tmem_st16_async(tSw + 16 * h, pk);
         }
-        // P (bf16) over the first 32 columns of its scores, the A operand of P V
-        tmem_st32_async(tS + lo + (g & 1) * KT, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(b_pf(g & 1));
-        if (bad_v) {
-          // A node that a row may not see can hold anything, and 0 times a
-          // non-finite value is not 0: such value rows are zeros in the tile
-          // and reach the rows that see them here.
-          wt = mbar_wait(b_od(g & 1), (g >> 1) & 1, a.err, 20);
-          if (!__all_sync(0xffffffffu, wt)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const int k0 = (t - p.ct) * KT;
-          const bf16* v = qkv + (int64_t(p.b) * a.N + k0) * a.ld_qkv + int64_t(a.H + a.Hkv + p.hk) * D;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            float f[32];
-            tmem_ld32_async(tO + lo + c, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
-#pragma unroll 1
-            for (int key = 0; key < KT; ++key) {
-              if (!((bad_v >> key) & 1)) continue;
-              float pj = 0.f;
-#pragma unroll
-              for (int i = 0; i < 64; i += 2) {
-                const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&pk[i >> 1]);
-                if (i == key) pj = __bfloat162float(h.x);
-                if (i + 1 == key) pj = __bfloat162float(h.y);
-              }
-              if (pj != 0.f)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  f[i] = fmaf(pj, __bfloat162float(v[key * a.ld_qkv + c + i]), f[i]);
-            }
-            tmem_st32(tO + lo + c, f);
-          }
-          tc_fence_before();
-        }
+        mbar_arrive(b_pf(buf_of(g)));
       }
       if (!ok) break;
-      const Piece done = p;
-      have = pieces.next(p);
-      if (have) load_q(p);  // the next piece's scores overlap this one's results
+      wait(b_listed(k + 1), ((k + 1) / kListed) & 1, 26);
       if (!ok) break;
-      const int last = g - 1;
-      bool wt = mbar_wait(b_od(last & 1), (last >> 1) & 1, a.err, 19);
-      if (!__all_sync(0xffffffffu, wt)) break;
-      if (!busy) continue;
+      if (list[(k + 1) % kListed].kt > 0)
+        load_q(list[(k + 1) % kListed]);  // the next piece's scores overlap this one's results
+      wait(b_od(buf_of(g - 1)), par_of(g - 1), 19);
+      if (!ok) break;
       tc_fence_after();
-      const bool whole = done.whole();
-      const float inv = 1.f / l;
-      bf16* out = static_cast<bf16*>(a.out) + (int64_t(done.b) * a.N + node) * a.ld_out + int64_t(hq) * D;
-      float* w = a.ws + pieces.slot(done) * slot_floats<MR>(D);
+      const bool whole = p.whole();
+      const int hq = p.hk * a.G + gr % a.G;
+      bf16* out = static_cast<bf16*>(a.out) + (int64_t(p.b) * a.N + node) * a.ld_out + int64_t(hq) * D;
+      float* w = a.ws + p.slot * slot_floats<MR>(D);
+      const float inv = whole ? 1.f / l : 1.f;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
+        if (!busy) break;
         uint32_t o[32];
-        tmem_ld32_async(tO + lo + c, o);
+        tmem_ld32_async(tOw + c, o);
         tmem_wait_ld(o);
         if (!real) continue;
         if (whole) {
@@ -449,17 +498,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(w + int64_t(e) * D + c + i) =
+            *reinterpret_cast<uint4*>(w + int64_t(row) * D + c + i) =
                 make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
       tc_fence_before();
       if (real) {
         if (whole) {
-          if (a.lse) a.lse[(int64_t(done.b) * a.H + hq) * a.N + node] = (m + log2f(l)) * kLn2;
+          if (a.lse) a.lse[(int64_t(p.b) * a.H + hq) * a.N + node] = (m + log2f(l)) * kLn2;
         } else {
-          w[MR * D + e] = m;
-          w[MR * D + MR + e] = l;
+          w[MR * D + row] = m;
+          w[MR * D + MR + row] = l;
+        }
+        if (any_bad) {
+          if (whole)
+            add_nonfinite<bf16, bf16>(a, p.b, p.hk, hq, node, pn, bad, mask, m, inv, out, 0, D);
+          else
+            add_nonfinite<bf16, float>(a, p.b, p.hk, hq, node, pn, bad, mask, m, 1.f,
+                                       w + int64_t(row) * D, 0, D);
         }
       }
     }
@@ -498,5 +554,5 @@ size_t tree_attn_tc_workspace(int B, int N, int H, int Hkv, int D) {
 }
 
 int launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t st) {
-  return a.D == 64 ? launch_tc<64>(a, st) : launch_tc<128>(a, st);
+  return a.D == 128 ? launch_tc<128>(a, st) : launch_tc<64>(a, st);
 }

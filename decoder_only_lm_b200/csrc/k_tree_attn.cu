@@ -76,7 +76,9 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_c
       *reinterpret_cast<float4*>(&sm.q[rr * LD + c * 4]) = f;
     }
     if (a.parent && t1 > ct && mask_of != b) {
-      build_masks(a.parent + int64_t(b) * a.N, s.n, sm.mask, sm.up, &sm.flag, a.err, tid, kThreads,
+      Parents parents;
+      parents.load(a.parent + int64_t(b) * a.N, s.n, tid, kThreads);
+      build_masks(parents, s.n, sm.mask, sm.up, &sm.flag, a.err, tid, kThreads,
                   [] { __syncthreads(); });
       mask_of = b;
     }

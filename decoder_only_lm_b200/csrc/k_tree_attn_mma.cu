@@ -129,12 +129,12 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
     fence_mbar_init();
     fence_proxy_async();
   }
+  typename S::Pieces pieces{&a, table, 0, 0, 0, 0, 0, 0, 0};
+  if (warp == NW) pieces = S::plan(a, table, true);
   __syncthreads();
 
   if (warp == NW) {
     // ------------------------------------------------ loads
-    auto pieces = S::plan(a, table, true);
-    __syncwarp();
     if (lane) return;
     int g = 0;
     bool ok = true;
@@ -215,11 +215,9 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         q[k][2 + h] = real ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
       }
     }
-    if (a.parent && p.t1 > p.ct && mask_of != p.b) {
-      sync();  // the last piece's masks are read no more
-      build_masks(a.parent + int64_t(p.b) * a.N, p.n, mask, up, flag, a.err, tid, 32 * NW, sync);
-      mask_of = p.b;
-    }
+    const bool new_masks = a.parent && p.t1 > p.ct && mask_of != p.b;
+    Parents parents;  // in flight until the nodes' tiles are reached
+    if (new_masks) parents.load(a.parent + int64_t(p.b) * a.N, p.n, tid, 32 * NW);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[DT][4];
 #pragma unroll
@@ -245,8 +243,12 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         if (fresh) {
           uint64_t* word = bad + (k0 >> 6);
           if (t == max(p.t0, p.ct)) {  // the piece's first: no other tile's words count
-            sync();                    // (the last piece's have been read)
+            sync();                    // (the last piece's words and masks have been read)
             if (tid < kMaxNodes / 64) bad[tid] = 0;
+            if (new_masks) {
+              build_masks(parents, p.n, mask, up, flag, a.err, tid, 32 * NW, sync);
+              mask_of = p.b;
+            }
             sync();
           }
           for (int e = tid; e < KT * C; e += 32 * NW) {

@@ -49,7 +49,7 @@ struct Cfg {
   static constexpr int kTile = KC * kChunk;      // a K (or V) tile
   static constexpr int NS = D == 64 ? 5 : 2;     // stages of K + V
   static constexpr int kMasks = kMaxNodes * (kMaskWords + 1) * 4;
-  static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + 1152 + 1024;
+  static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + 1280 + 1024;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -110,16 +110,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t* mask = reinterpret_cast<uint32_t*>(ring + NS * 2 * F::kTile);
   int* up = reinterpret_cast<int*>(mask + kMaxNodes * kMaskWords);
   uint64_t* bars = reinterpret_cast<uint64_t*>(up + kMaxNodes);
-  // q_full | kv_full[NS] | kv_empty[NS] | s_full[2] | p_full[2] | o_done[2] | rows | listed[kListed]
-  const uint32_t b_q = smem_u32(bars);
-  auto b_kvf = [&](int s) { return smem_u32(bars + 1 + s); };
-  auto b_kve = [&](int s) { return smem_u32(bars + 1 + NS + s); };
-  auto b_sf = [&](int i) { return smem_u32(bars + 1 + 2 * NS + i); };
-  auto b_pf = [&](int i) { return smem_u32(bars + 3 + 2 * NS + i); };
-  auto b_od = [&](int i) { return smem_u32(bars + 5 + 2 * NS + i); };
-  const uint32_t b_rows = smem_u32(bars + 7 + 2 * NS);
-  auto b_listed = [&](int k) { return smem_u32(bars + 8 + 2 * NS + k % kListed); };
-  Listed* list = reinterpret_cast<Listed*>(bars + 8 + 2 * NS + kListed);
+  // k_full[NS] | v_full[NS] | k_empty[NS] | v_empty[NS] | q_full | s_full[2] | p_full[2] |
+  // o_done[2] | rows | listed[kListed]
+  auto b_kf = [&](int s) { return smem_u32(bars + s); };
+  auto b_vf = [&](int s) { return smem_u32(bars + NS + s); };
+  auto b_ke = [&](int s) { return smem_u32(bars + 2 * NS + s); };
+  auto b_ve = [&](int s) { return smem_u32(bars + 3 * NS + s); };
+  const uint32_t b_q = smem_u32(bars + 4 * NS);
+  auto b_sf = [&](int i) { return smem_u32(bars + 4 * NS + 1 + i); };
+  auto b_pf = [&](int i) { return smem_u32(bars + 4 * NS + 3 + i); };
+  auto b_od = [&](int i) { return smem_u32(bars + 4 * NS + 5 + i); };
+  const uint32_t b_rows = smem_u32(bars + 4 * NS + 7);
+  auto b_listed = [&](int k) { return smem_u32(bars + 4 * NS + 8 + k % kListed); };
+  Listed* list = reinterpret_cast<Listed*>(bars + 4 * NS + 8 + kListed);
   uint64_t* bad = reinterpret_cast<uint64_t*>(list + kListed);  // nodes of non-finite values
   uint32_t* flag = reinterpret_cast<uint32_t*>(bad + kMaxNodes / 64);
   uint32_t* slot = flag + 1;
@@ -134,8 +137,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(b_q, 1);
     mbar_init(b_rows, MR);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(b_kvf(s), 1);
-      mbar_init(b_kve(s), 1);
+      mbar_init(b_kf(s), 1);
+      mbar_init(b_vf(s), 1);
+      mbar_init(b_ke(s), 1);
+      mbar_init(b_ve(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sf(i), 1);
@@ -148,6 +153,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncwarp();
   if (warp == 1) tmem_alloc(smem_u32(slot), kTmemCols);
+  typename Split<MR, KT>::Pieces pieces{&a, table, 0, 0, 0, 0, 0, 0, 0};
+  if (warp == 0) pieces = Split<MR, KT>::plan(a, table, true);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -157,12 +164,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 0) {
     // ------------------------------------------------ plan, loads
-    auto pieces = Split<MR, KT>::plan(a, table, true);
-    __syncwarp();
     if (lane == 0) {
       int s = 0;          // stage, and how often the ring has come round
       uint32_t round = 0;
-      int filled = 0;
+      int filled_k = 0, filled = 0;  // keys', values' fills
       bool ok = true;
       for (int k = 0; ok; ++k) {
         Listed& p = list[k % kListed];
@@ -178,20 +183,28 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (q.kt == 0) break;
         const int row0 = (q.b * a.Hkv + q.hk) * a.Tc;  // rows of the caches fit 31 bits
         for (int t = q.t0; t < q.t1; ++t) {
-          if (!mbar_wait(b_kve(s), (round & 1) ^ 1, a.err, 11)) {
-            ok = false;
-            break;
-          }
           const bool fresh = t >= q.ct;
           const uint32_t dk = sKV + s * 2 * F::kTile, dv = dk + F::kTile;
           const int y = fresh ? q.b * a.N + (t - q.ct) * KT : row0 + t * KT;
           const int xk = fresh ? (a.H + q.hk) * D : 0, xv = fresh ? xk + a.Hkv * D : 0;
-          mbar_expect_tx(b_kvf(s), 2 * F::kTile);
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            tma_load_2d(dk + c * F::kChunk, fresh ? &mx : &mk, b_kvf(s), xk + 64 * c, y);
-            tma_load_2d(dv + c * F::kChunk, fresh ? &mx : &mv, b_kvf(s), xv + 64 * c, y);
+          // keys go when the tile's scores are done, values only after its product
+          if (!mbar_wait(b_ke(s), (round & 1) ^ 1, a.err, 11)) {
+            ok = false;
+            break;
           }
+          mbar_expect_tx(b_kf(s), F::kTile);
+#pragma unroll
+          for (int c = 0; c < KC; ++c)
+            tma_load_2d(dk + c * F::kChunk, fresh ? &mx : &mk, b_kf(s), xk + 64 * c, y);
+          ++filled_k;
+          if (!mbar_wait(b_ve(s), (round & 1) ^ 1, a.err, 11)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(b_vf(s), F::kTile);
+#pragma unroll
+          for (int c = 0; c < KC; ++c)
+            tma_load_2d(dv + c * F::kChunk, fresh ? &mx : &mv, b_vf(s), xv + 64 * c, y);
           ++filled;
           if (++s == NS) {
             s = 0;
@@ -200,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       // every issued copy has landed before the CTA may exit
-      for (int q = max(0, filled - NS); q < filled; ++q) mbar_wait(b_kvf(q % NS), (q / NS) & 1, a.err, 15);
+      for (int q = max(0, filled_k - NS); q < filled_k; ++q) mbar_wait(b_kf(q % NS), (q / NS) & 1, a.err, 15);
+      for (int q = max(0, filled - NS); q < filled; ++q) mbar_wait(b_vf(q % NS), (q / NS) & 1, a.err, 15);
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA
@@ -213,14 +227,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t dV = desc_mnmajor(sKV + F::kTile, 0);
     const uint32_t uS = uniform(tS), uO = uniform(tO);
     int g = 0, s = 0, last = 0;  // tile, its stage, the stage of the tile before
-    uint32_t round = 0;
+    uint32_t round = 0, last_round = 0;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, int where) {
       const bool w = mbar_wait(bar, parity, a.err, where);
       if (!__all_sync(0xffffffffu, w)) ok = false;
     };
     // O += P V of tile gt in stage st
-    auto issue_pv = [&](int gt, int st, bool acc) {
+    auto issue_pv = [&](int gt, int st, uint32_t rd, bool acc) {
+      wait(b_vf(st), rd & 1, 13);
       wait(b_pf(buf_of(gt)), par_of(gt), 13);
       if (!ok) return;
       tc_fence_after();
@@ -234,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 1; i < 4; ++i) umma_ts_i<1>(uO, pa + 8 * i, v + i * 128, id_o);
         umma_commit(b_od(buf_of(gt)));
-        umma_commit(b_kve(st));
+        umma_commit(b_ve(st));
       }
       __syncwarp();
     };
@@ -247,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int t = t0; ok && t < t1; ++t, ++g) {
         // (the scores' buffer is free: it held the probabilities of tile g - 2,
         // whose product was issued before this)
-        wait(b_kvf(s), round & 1, 12);
+        wait(b_kf(s), round & 1, 12);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -265,16 +280,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 umma_i<1>(ts, qa, kb, id_s);
             }
           umma_commit(b_sf(buf_of(g)));
+          umma_commit(b_ke(s));
         }
         __syncwarp();
-        if (t > t0) issue_pv(g - 1, last, t - 1 > t0);
+        if (t > t0) issue_pv(g - 1, last, last_round, t - 1 > t0);
         last = s;
+        last_round = round;
         if (++s == NS) {
           s = 0;
           ++round;
         }
       }
-      if (ok) issue_pv(g - 1, last, t1 - 1 > t0);
+      if (ok) issue_pv(g - 1, last, last_round, t1 - 1 > t0);
     }
     // all issued MMAs complete before TMEM is released
     if (g > 0) mbar_wait(b_od(buf_of(g - 1)), par_of(g - 1), a.err, 16);
@@ -325,17 +342,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int s = gt % NS;
       const bool fresh = t >= q.ct;
       const int nk = fresh ? q.n - (t - q.ct) * KT : q.len - t * KT;
-      wait(b_kvf(s), (gt / NS) & 1, 21);  // complete: its scores are
+      wait(b_vf(s), (gt / NS) & 1, 21);
       uint8_t* v = ring + s * 2 * F::kTile + F::kTile;
       uint64_t drop = nk >= KT ? 0 : ~uint64_t(0) << nk;
       bool found = false;
       if (fresh) {
         uint64_t* word = bad + (t - q.ct);
-        if (t == max(q.t0, q.ct)) {  // the piece's first: no other tile's words count
-          rows_sync();               // (the last piece's have been read)
-          if (row < kMaxNodes / 64) bad[row] = 0;
-          rows_sync();
-        }
         for (int x = row; x < KT * D / 8; x += MR) {  // 16-byte units, the swizzle left alone
           const int r = x / 8 % KT;
           const uint4 u = *reinterpret_cast<const uint4*>(v + x * 16);
@@ -365,15 +377,25 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool real = row < rows;
       const bool busy = (row & ~31) < rows;  // some row of this warp is real
       const int gr = p.rt * MR + (real ? row : 0), node = gr / a.G;
-      if (a.parent && t1 > ct && mask_of != p.b) {
-        build_masks(a.parent + int64_t(p.b) * a.N, pn, mask, up, flag, a.err, row, MR, rows_sync);
-        mask_of = p.b;
-      }
+      const bool new_masks = a.parent && t1 > ct && mask_of != p.b;
+      Parents parents;  // in flight until the nodes' tiles are reached
+      if (new_masks) parents.load(a.parent + int64_t(p.b) * a.N, pn, row, MR);
       bool any_bad = false, first = true;
       float m = -INFINITY, l = 0.f;
       for (int t = p.t0; t < t1; ++t, ++g, first = false) {
         wait(b_sf(buf_of(g)), par_of(g), 14);
-        if ((t + 1) * KT > len) any_bad |= clear(p, t, g);
+        if ((t + 1) * KT > len) {
+          if (t == max(p.t0, ct)) {  // the piece's first node tile
+            rows_sync();             // (the last piece's words and masks have been read)
+            if (row < kMaxNodes / 64) bad[row] = 0;
+            if (new_masks) {
+              build_masks(parents, pn, mask, up, flag, a.err, row, MR, rows_sync);
+              mask_of = p.b;
+            }
+            rows_sync();
+          }
+          any_bad |= clear(p, t, g);
+        }
         if (!ok) break;
         if (!busy) {
           mbar_arrive(b_pf(buf_of(g)));

@@ -72,13 +72,14 @@ struct Split {
 
   // The pieces of a CTA's run in order.
   struct Pieces {
-    const TreeAttnArgs& a;
+    const TreeAttnArgs* args;
     const SeqDims* table;  // lengths of sequences b0 .. b0 + 31
     int64_t pos, end, total, first;
     int ctas;  // CTAs with a run: never more than places, so that none is empty
     int b0, b;
     // (false: the run is done, p holds nothing)
     __device__ __forceinline__ bool next(Piece& p) {
+      const TreeAttnArgs& a = *args;
       while (pos < end) {
         const SeqDims s = b - b0 < kTable ? table[b - b0] : seq_dims(a, b);
         const int64_t n = tiles(a, s);
@@ -119,6 +120,7 @@ struct Split {
     // By the CTA in whose run the segment begins: the first and last CTA that
     // hold a piece of it (place x is CTA ((x + 1) ctas - 1) / total's).
     __device__ __forceinline__ void note(const Piece& p) const {
+      const TreeAttnArgs& a = *args;
       const int rts = ceil_div(a.N * a.G, MR);
       a.seg[(int64_t(p.b) * a.Hkv + p.hk) * rts + p.rt] =
           make_int2(int(blockIdx.x), p.whole() ? int(blockIdx.x) : last_cta(p.s0 + p.kt));
@@ -139,7 +141,7 @@ struct Split {
     bool bad = false;
     int64_t total = 0, first = 0, base = 0;
     int b0 = a.B;
-    Pieces q{a, table, 0, 0, 1, 0, 0, 0, 0};
+    Pieces q{&a, table, 0, 0, 1, 0, 0, 0, 0};
     auto scan = [&](int64_t v) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -205,19 +207,31 @@ struct Listed : Piece {
 // up to kWalk steps; what is left of deeper trees goes by doubling, mask(i) |=
 // mask(up(i)), up(i) = up(up(i)).  By the `threads` threads that call it (>=
 // kMaxNodes / 2; thread tid of them), with `sync` their barrier; flag is a word
-// of shared memory.  A parent outside [-1, i) counts as -1 and is reported.
+// of shared memory.  The thread's parents come in registers (see Parents), loaded
+// long before.  A parent outside [-1, i) counts as -1 and is reported.
 constexpr int kWalk = 16;
+struct Parents {
+  int p[2];
+  __device__ __forceinline__ void load(const int32_t* parent, int n, int tid, int threads) {
+    p[0] = tid < n ? parent[tid] : -1;
+    p[1] = tid + threads < n ? parent[tid + threads] : -1;
+  }
+};
 template <typename Sync>
-__device__ __forceinline__ void build_masks(const int32_t* parent, int n, uint32_t* mask, int* up,
+__device__ __forceinline__ void build_masks(const Parents& parents, int n, uint32_t* mask, int* up,
                                             uint32_t* flag, int* err, int tid, int threads,
                                             Sync sync) {
-  for (int i = tid; i < n; i += threads) {
-    int p = parent[i];
-    if (p < -1 || p >= i) {
-      atomicExch(err, kTreeBadInput);
-      p = -1;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + k * threads;
+    int p = parents.p[k];
+    if (i < n) {
+      if (p < -1 || p >= i) {
+        atomicExch(err, kTreeBadInput);
+        p = -1;
+      }
+      up[i] = p;
     }
-    up[i] = p;
   }
   if (tid == 0) *flag = 0;
   sync();

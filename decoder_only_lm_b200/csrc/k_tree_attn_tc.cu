@@ -16,7 +16,12 @@
 //                     when a maximum grows by more than 2^8, results at a
 //                     piece's end.
 // S has two buffers, so that the next tile's scores are there when a softmax
-// ends.
+// ends.  A softmax is a chain of latencies (scores from TMEM, exponentials,
+// probabilities to TMEM) that grows with the keys a thread takes, and with few
+// rows most lanes would be idle: up to 64 (32) rows are held P = 2 (4) times, in
+// lanes row + 64 (32) i, and copy i takes its share of each tile's keys, with
+// zeros for the others among its probabilities, so the products stay the same
+// instructions.  The copies' maxima, sums and outputs merge at a piece's end.
 // What a tile holds behind the last key (or the last node) is not the
 // sequence's: its scores are masked, and the row threads clear its value rows
 // before the product.  They also bring the query rows, the next piece's before
@@ -35,21 +40,25 @@ using namespace tree;
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int MR = 128;      // query rows of a tile = TMEM lanes = row threads
+constexpr int kLanes = 128;  // TMEM lanes = row threads
 constexpr int KT = 64;       // keys of a tile
 constexpr int kTmemCols = 256;
 constexpr float kRescale = 8.f;  // lazy-rescale threshold, log2 units
 
-template <int D>
+template <int D, int P>
 struct Cfg {
+  static constexpr int MR = kLanes / P;          // query rows of a tile
   static constexpr int KC = D / 64;              // 64-channel chunks of a row
-  static constexpr int kChunkQ = MR * 128;   // 16 KB: 128 rows x 64 bf16
+  static constexpr int kChunkQ = kLanes * 128;   // 16 KB: 128 rows x 64 bf16
   static constexpr int kChunk = KT * 128;        // 8 KB: 64 rows x 64 bf16
   static constexpr int kQ = KC * kChunkQ;
   static constexpr int kTile = KC * kChunk;      // a K (or V) tile
-  static constexpr int NS = D == 64 ? 5 : 2;     // stages of K + V
-  static constexpr int kMasks = kMaxNodes * (kMaskWords + 1) * 4;
-  static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + 1280 + 1024;
+  static constexpr int NS = D == 128 ? 2 : P > 1 ? 4 : 5;  // stages of K + V
+  static constexpr int kNodes = P > 1 ? MR : kMaxNodes;   // a node has a row at least
+  static constexpr int kMasks = kNodes * (kMaskWords + 1) * 4;
+  static constexpr int LX = 20;                  // row stride of the copies' exchange
+  static constexpr int kExchange = P > 1 ? kLanes * (LX + 2) * 4 : 0;
+  static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + kExchange + 1280 + 1024;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -81,6 +90,12 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8_async(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -95,21 +110,23 @@ __device__ __forceinline__ T uniform(T v) {
 // Tile t of a piece is wholly cached: no key of it is masked.
 __device__ __forceinline__ bool plain(const Piece& p, int t) { return (t + 1) * KT <= p.len; }
 
-template <int D>
+template <int D, int P>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                         const __grid_constant__ CUtensorMap mx,
                         const __grid_constant__ TreeAttnArgs a) {
-  using F = Cfg<D>;
-  constexpr int NS = F::NS, KC = F::KC;
+  using F = Cfg<D, P>;
+  constexpr int NS = F::NS, KC = F::KC, MR = F::MR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* ring = smem + F::kQ;
   const uint32_t sQ = smem_u32(smem), sKV = smem_u32(ring);
   uint32_t* mask = reinterpret_cast<uint32_t*>(ring + NS * 2 * F::kTile);
-  int* up = reinterpret_cast<int*>(mask + kMaxNodes * kMaskWords);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(up + kMaxNodes);
+  int* up = reinterpret_cast<int*>(mask + F::kNodes * kMaskWords);
+  float* xch = reinterpret_cast<float*>(up + F::kNodes);  // 16 outputs a lane, for the other copies
+  float2* ml = reinterpret_cast<float2*>(xch + kLanes * F::LX);  // ... maximum and sum
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(up + F::kNodes) + F::kExchange);
   // k_full[NS] | v_full[NS] | k_empty[NS] | v_empty[NS] | q_full | s_full[2] | p_full[2] |
   // o_done[2] | rows | listed[kListed]
   auto b_kf = [&](int s) { return smem_u32(bars + s); };
@@ -135,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 32) {
     mbar_init(b_q, 1);
-    mbar_init(b_rows, MR);
+    mbar_init(b_rows, kLanes);
     for (int s = 0; s < NS; ++s) {
       mbar_init(b_kf(s), 1);
       mbar_init(b_vf(s), 1);
@@ -144,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sf(i), 1);
-      mbar_init(b_pf(i), MR);
+      mbar_init(b_pf(i), kLanes);
       mbar_init(b_od(i), 1);
     }
     for (int k = 0; k < kListed; ++k) mbar_init(b_listed(k), 1);
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // warp-uniform (from one lane's branch every operand of an MMA has to be moved
     // to the uniform registers first), and one elected lane issues.
     const bool leader = elect_one();
-    const uint32_t id_s = idesc_bf16(MR, KT, 0, 0), id_o = idesc_bf16(MR, D, 0, 1);
+    const uint32_t id_s = idesc_bf16(kLanes, KT, 0, 0), id_o = idesc_bf16(kLanes, D, 0, 1);
     const uint64_t dQ = desc_kmajor(sQ, 0), dK = desc_kmajor(sKV, 0);
     const uint64_t dV = desc_mnmajor(sKV + F::kTile, 0);
     const uint32_t uS = uniform(tS), uO = uniform(tO);
@@ -297,7 +314,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (g > 0) mbar_wait(b_od(buf_of(g - 1)), par_of(g - 1), a.err, 16);
   } else {
     // ------------------------------------------------ rows
-    const int row = (warp & 3) * 32 + lane;  // of the tile; TMEM lane
+    constexpr int NC = KT / P;               // keys of a tile that a copy takes
+    constexpr int CW = NC < 32 ? NC : 32;    // ... at a time
+    const int e = (warp & 3) * 32 + lane;    // TMEM lane
+    const int row = e % MR, copy = e / MR;   // of the tile
     const uint32_t lo = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tOw = tO + lo;            // this lane's output
     const float scale = rsqrtf(float(D)) * kLog2e;
@@ -329,11 +349,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int c = 0; c < 8; ++c) v[c] = real ? src[c0 + c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(smem + (c0 >> 3) * F::kChunkQ + row * 128 + ((c ^ (row & 7)) << 4)) = v[c];
+          *reinterpret_cast<uint4*>(smem + (c0 >> 3) * F::kChunkQ + e * 128 + ((c ^ (e & 7)) << 4)) = v[c];
       }
       fence_proxy_async();  // visible to the MMAs
       rows_sync();
-      if (row == 0) mbar_arrive(b_q);
+      if (e == 0) mbar_arrive(b_q);
     };
     // A tile with foreign rows, or with nodes that a row may not see: value rows
     // behind the last key become 0, and so do node rows with non-finite values,
@@ -348,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool found = false;
       if (fresh) {
         uint64_t* word = bad + (t - q.ct);
-        for (int x = row; x < KT * D / 8; x += MR) {  // 16-byte units, the swizzle left alone
+        for (int x = e; x < KT * D / 8; x += kLanes) {  // 16-byte units, the swizzle left alone
           const int r = x / 8 % KT;
           const uint4 u = *reinterpret_cast<const uint4*>(v + x * 16);
           auto inf = [](uint32_t w2) {
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         drop |= *word;
       }
       if (drop) {
-        for (int x = row; x < KT * D / 8; x += MR)
+        for (int x = e; x < KT * D / 8; x += kLanes)
           if ((drop >> (x / 8 % KT)) & 1) *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async();  // before this thread's arrival that the product waits for
       }
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int gr = p.rt * MR + (real ? row : 0), node = gr / a.G;
       const bool new_masks = a.parent && t1 > ct && mask_of != p.b;
       Parents parents;  // in flight until the nodes' tiles are reached
-      if (new_masks) parents.load(a.parent + int64_t(p.b) * a.N, pn, row, MR);
+      if (new_masks) parents.load(a.parent + int64_t(p.b) * a.N, pn, e, kLanes);
       bool any_bad = false, first = true;
       float m = -INFINITY, l = 0.f;
       for (int t = p.t0; t < t1; ++t, ++g, first = false) {
@@ -387,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if ((t + 1) * KT > len) {
           if (t == max(p.t0, ct)) {  // the piece's first node tile
             rows_sync();             // (the last piece's words and masks have been read)
-            if (row < kMaxNodes / 64) bad[row] = 0;
+            if (e < kMaxNodes / 64) bad[e] = 0;
             if (new_masks) {
-              build_masks(parents, pn, mask, up, flag, a.err, row, MR, rows_sync);
+              build_masks(parents, pn, mask, up, flag, a.err, e, kLanes, rows_sync);
               mask_of = p.b;
             }
             rows_sync();
@@ -411,33 +431,38 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (nk < KT) see = (uint64_t(1) << nk) - 1;
           if (fresh) see &= sees(!a.parent, mask, node, k0);
         }
-        // Two halves of 32 keys: x = raw scores, keys that the row may not see
-        // -inf.  The base m of the probabilities (log2 domain) follows the
-        // maximum only when it grows by more than 2^8 (they stay <= 256); 0 is
-        // used while the row has seen nothing (every p is then 2^(-inf) = 0).
+        // This copy's keys, up to 32 at a time: x = raw scores, keys that the row may
+        // not see -inf.  The base m of the probabilities (log2 domain) follows the
+        // maximum only when it grows by more than 2^8 (they stay <= 256); 0 is used
+        // while the row has seen nothing (every p is then 2^(-inf) = 0).
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          tmem_ld32_async(tSw + 32 * h, r);
-          tmem_wait_ld(r);
-          float x[32];
+        for (int h = 0; h < NC / CW; ++h) {
+          const int key0 = copy * NC + h * CW;
+          float x[CW];
+          if constexpr (CW == 32) {
+            uint32_t r[32];
+            tmem_ld32_async(tSw + key0, r);
+            tmem_wait_ld(r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-          if (!open) {
-            const uint32_t bits = uint32_t(see >> (32 * h));
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1 ? x[i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+          } else {
+            tmem_ld16(tSw + key0, x);
           }
-          float c2[2];
+          if (!open) {
+            const uint32_t bits = uint32_t(see >> key0);
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
+            for (int i = 0; i < CW; ++i) x[i] = (bits >> i) & 1 ? x[i] : -INFINITY;
+          }
+          float c2[CW / 16];
+#pragma unroll
+          for (int k2 = 0; k2 < CW / 16; ++k2) {
             const float* y = x + 16 * k2;
             float mm = max3f(y[0], y[1], y[2]);
 #pragma unroll
             for (int i = 3; i < 15; i += 2) mm = max3f(mm, y[i], y[i + 1]);
             c2[k2] = fmaxf(mm, y[15]);
           }
-          const float mn = __fmul_rn(fmaxf(c2[0], c2[1]), scale);
+          const float mn = __fmul_rn(fmaxf(c2[0], c2[CW / 16 - 1]), scale);
           const bool resc = mn > m + kRescale;
           if (__any_sync(0xffffffffu, resc)) {
             const float corr = resc ? ex2(m - mn) : 1.f;
@@ -454,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               tmem_st16_async(tSw, q);
             }
-            if (!first) {  // O holds the last step's product
+            if (!first) {  // O holds the last tile's product
               wait(b_od(buf_of(g - 1)), par_of(g - 1), 17);
               tc_fence_after();
 #pragma unroll 1
@@ -468,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-          uint32_t pk[16];
+          uint32_t pk[CW / 2];
           float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < CW; i += 2) {
             float u0, u1;
             fma2(u0, u1, x[i], x[i + 1], scale, scale, -base, -base);
             const float p0 = ex2(u0), p1 = ex2(u1);
@@ -479,9 +504,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             pk[i >> 1] = pack2(p0, p1);
           }
           l += (sa[0] + sb[0]) + (sa[1] + sb[1]);
-          // P (bf16) over the first 32 columns of its scores, the A operand of
-          // P V: a half's 16 columns were read by the first load
-          tmem_st16_async(tSw + 16 * h, pk);
+          // P (bf16) over the first 32 columns of its scores, the A operand of P V:
+          // what it overwrites has been read; zeros for the other copies' keys
+          if constexpr (P == 1) {
+            tmem_st16_async(tSw + 16 * h, pk);
+          } else {
+            uint32_t zero[CW / 2];
+#pragma unroll
+            for (int i = 0; i < CW / 2; ++i) zero[i] = 0;
+#pragma unroll
+            for (int c = 0; c < P; ++c) {
+              const uint32_t at = tSw + ((copy + c) % P) * (CW / 2);
+              if constexpr (P == 2)
+                tmem_st16_async(at, c == 0 ? pk : zero);
+              else
+                tmem_st8_async(at, c == 0 ? pk : zero);
+            }
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -499,46 +538,87 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int hq = p.hk * a.G + gr % a.G;
       bf16* out = static_cast<bf16*>(a.out) + (int64_t(p.b) * a.N + node) * a.ld_out + int64_t(hq) * D;
       float* w = a.ws + p.slot * slot_floats<MR>(D);
-      const float inv = whole ? 1.f / l : 1.f;
+      float M = m, L = l, f = 1.f;
+      if constexpr (P > 1) {  // over the row's copies
+        ml[e] = make_float2(m, l);
+        rows_sync();
+        L = 0.f;
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        if (!busy) break;
-        uint32_t o[32];
-        tmem_ld32_async(tOw + c, o);
-        tmem_wait_ld(o);
-        if (!real) continue;
+        for (int c = 0; c < P; ++c) M = fmaxf(M, ml[row + c * MR].x);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          const float2 u = ml[row + c * MR];
+          L += u.x == -INFINITY ? 0.f : ex2(u.x - M) * u.y;
+        }
+        f = m == -INFINITY ? 0.f : ex2(m - M);
+      }
+      if (whole) f /= L;
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        float x[16];
+        if (busy) {
+          tmem_ld16(tOw + c, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= f;
+        }
+        if constexpr (P > 1) {
+          // 16 columns at a time; the copies finish them in turn
+          if (busy) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(xch + e * F::LX + i) =
+                  make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          }
+          rows_sync();
+          if (busy && copy == (c / 16) % P) {
+#pragma unroll
+            for (int k2 = 1; k2 < P; ++k2) {
+              const float* y = xch + (row + (copy + k2) % P * MR) * F::LX;
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(y + i);
+                x[i] += v.x;
+                x[i + 1] += v.y;
+                x[i + 2] += v.z;
+                x[i + 3] += v.w;
+              }
+            }
+          }
+          rows_sync();
+        }
+        if (!real || copy != (c / 16) % P) continue;
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 v;
-            v.x = pack2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-            v.y = pack2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-            v.z = pack2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-            v.w = pack2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-            *reinterpret_cast<uint4*>(out + c + i) = v;
-          }
+          for (int i = 0; i < 16; i += 8)
+            *reinterpret_cast<uint4*>(out + c + i) =
+                make_uint4(pack2(x[i], x[i + 1]), pack2(x[i + 2], x[i + 3]), pack2(x[i + 4], x[i + 5]),
+                           pack2(x[i + 6], x[i + 7]));
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(w + int64_t(row) * D + c + i) =
-                make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(w + int64_t(row) * D + c + i) =
+                make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         }
       }
+      if (!ok) break;
       tc_fence_before();
       if (real) {
-        if (whole) {
-          if (a.lse) a.lse[(int64_t(p.b) * a.H + hq) * a.N + node] = (m + log2f(l)) * kLn2;
-        } else {
-          w[MR * D + row] = m;
-          w[MR * D + MR + row] = l;
+        if (copy == 0) {
+          if (whole) {
+            if (a.lse) a.lse[(int64_t(p.b) * a.H + hq) * a.N + node] = (M + log2f(L)) * kLn2;
+          } else {
+            w[MR * D + row] = M;
+            w[MR * D + MR + row] = L;
+          }
         }
-        if (any_bad) {
-          if (whole)
-            add_nonfinite<bf16, bf16>(a, p.b, p.hk, hq, node, pn, bad, mask, m, inv, out, 0, D);
-          else
-            add_nonfinite<bf16, float>(a, p.b, p.hk, hq, node, pn, bad, mask, m, 1.f,
-                                       w + int64_t(row) * D, 0, D);
-        }
+        if (any_bad)
+          for (int c = 16 * copy; c < D; c += 16 * P) {  // the columns that this thread stored
+            if (whole)
+              add_nonfinite<bf16, bf16>(a, p.b, p.hk, hq, node, pn, bad, mask, M, 1.f / L, out, c, c + 16);
+            else
+              add_nonfinite<bf16, float>(a, p.b, p.hk, hq, node, pn, bad, mask, M, 1.f,
+                                         w + int64_t(row) * D, c, c + 16);
+          }
       }
     }
   }
@@ -550,9 +630,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 int grid_size() { return 2 * gpt2_internal::sm_count(); }
 
-template <int D>
+template <int D, int P>
 int launch_tc(const TreeAttnArgs& a, cudaStream_t st) {
-  using F = Cfg<D>;
+  using F = Cfg<D, P>;
   CUtensorMap mk, mv, mx;
   const int64_t rows = int64_t(a.B) * a.Hkv * a.Tc;
   if (!make_map_bf16(&mk, a.k, D, rows, D, KT) || !make_map_bf16(&mv, a.v, D, rows, D, KT) ||
@@ -560,21 +640,32 @@ int launch_tc(const TreeAttnArgs& a, cudaStream_t st) {
     gpt2_internal::set_error("tree_attention: tensor map encoding failed");
     return GPT2_ERR_CUDA;
   }
-  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_tc_kernel<D>,
+  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_tc_kernel<D, P>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem));
-  const TreeAttnArgs w = with_workspace<MR>(a, grid_size());
-  tree_attn_tc_kernel<D><<<grid_size(), kThreads, F::kSmem, st>>>(mk, mv, mx, w);
+  const TreeAttnArgs w = with_workspace<F::MR>(a, grid_size());
+  tree_attn_tc_kernel<D, P><<<grid_size(), kThreads, F::kSmem, st>>>(mk, mv, mx, w);
   COUNT_LAUNCH(1);
   GPT2_LAUNCH_CHECK();
-  return launch_combine<bf16, MR, D>(w, st);
+  return launch_combine<bf16, F::MR, D>(w, st);
 }
+
+// Copies of a row: as many as fit its tile's 128 lanes.
+int copies(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
 
 }  // namespace
 
 size_t tree_attn_tc_workspace(int B, int N, int H, int Hkv, int D) {
-  return workspace_bytes<MR>(grid_size(), B, N, H, Hkv, D);
+  switch (copies(N * (H / Hkv))) {
+    case 4: return workspace_bytes<32>(grid_size(), B, N, H, Hkv, D);
+    case 2: return workspace_bytes<64>(grid_size(), B, N, H, Hkv, D);
+    default: return workspace_bytes<128>(grid_size(), B, N, H, Hkv, D);
+  }
 }
 
 int launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t st) {
-  return a.D == 128 ? launch_tc<128>(a, st) : launch_tc<64>(a, st);
+  switch (copies(a.N * a.G)) {
+    case 4: return a.D == 128 ? launch_tc<128, 4>(a, st) : launch_tc<64, 4>(a, st);
+    case 2: return a.D == 128 ? launch_tc<128, 2>(a, st) : launch_tc<64, 2>(a, st);
+    default: return a.D == 128 ? launch_tc<128, 1>(a, st) : launch_tc<64, 1>(a, st);
+  }
 }

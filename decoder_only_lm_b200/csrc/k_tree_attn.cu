@@ -43,7 +43,7 @@ struct Smem {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_constant__ TreeAttnArgs a) {
-  using S = Split<MR, KT>;
+  using S = Split<MR, KT, 2>;
   constexpr int LD = Smem<D>::LD, LP = Smem<D>::LP;
   constexpr int V4 = D / 4;              // float4 of a row
   constexpr int NO = (V4 + 7) / 8;       // float4 of the output a thread holds
@@ -245,13 +245,13 @@ int launch_tree_attn_mma(const TreeAttnArgs& a, cudaStream_t st);
 size_t tree_attn_tc_workspace(int B, int N, int H, int Hkv, int D);
 int launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t st);
 
-// bf16 with head size 64 or 128 and more than kFewRows query rows per
-// key/value head: 5th-generation tensor cores.
-#include <cstdlib>
-static bool on_tc(int N, int H, int Hkv, int D) {
-  static const int kFewRows = getenv("TA_ROWS") ? atoi(getenv("TA_ROWS")) : 16;
-  return D >= 64 && N * (H / Hkv) > kFewRows;
-}
+// bf16 with head size 64 or 128 and more than 32 query rows per key/value head
+// goes to the 5th-generation tensor cores: their tile of 128 rows costs the same
+// however few are real, the warp-level instructions grow with the rows.  Measured
+// (head size 64, us, warp level / 5th generation): 16 sequences of 500-1000, 16
+// rows 18.5 / 21.6, 32 rows 22.3 / 23.5, 48 rows 26.4 / 23.8, 64 rows 27.7 / 24.8;
+// 4 sequences of 8-16 thousand, 32 rows 36.4 / 35.1, 48 rows 49.1 / 40.0.
+static bool on_tc(int N, int H, int Hkv, int D) { return D >= 64 && N * (H / Hkv) > 32; }
 
 size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16_in) {
   if (!bf16_in) return workspace_bytes<MR>(simt_grid(), B, N, H, Hkv, D);

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
     tree_attn_mma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                          const __grid_constant__ CUtensorMap mx, const __grid_constant__ TreeAttnArgs a) {
   using F = Cfg<D, WM, WK>;
-  using S = Split<F::MR, KT>;
+  using S = Split<F::MR, KT, 4>;  // (0, 2, 4, 6: 16.1, 13.0, 12.5, 13.1 us for 16 single tokens)
   constexpr int MR = F::MR, KW = F::KW, NS = F::NS, NW = F::NW;
   constexpr int NT = KW / 8;   // score tiles of 8 keys
   constexpr int DT = D / 8;    // output tiles of 8 channels
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
       mbar_init(b_empty(s), NW);
     }
     for (int k = 0; k < kListed; ++k) mbar_init(b_listed(k), 1);
-    mbar_init(b_rows, 32 * NW);
+    mbar_init(b_rows, NW);
     fence_mbar_init();
     fence_proxy_async();
   }
@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
   // leave the others waiting
   uint32_t syncs = 0;
   auto sync = [&] {
-    mbar_arrive(b_rows);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_rows);
     wait(b_rows, syncs++ & 1, 35);
   };
   const float scale = rsqrtf(float(D)) * kLog2e;
@@ -488,16 +489,19 @@ struct Variant {
 };
 
 // Rows of a key/value head decide how many warps cover rows: up to 16 rows all
-// four split the keys, up to 32 two, up to 64 none; beyond that eight warps
-// cover 128 rows, so that a cache tile is read half as often.
+// four split the keys, up to 32 two do.  More rows come here only with head sizes
+// 16 and 32: four warps for 64 rows, and eight for 128, so that a cache tile is
+// read half as often.
 template <typename Fn>
 auto pick(int D, int rows, Fn fn) {
   auto by_rows = [&](auto d) {
     constexpr int kD = decltype(d)::value;
     if (rows <= 16) return fn(Variant<kD, 1, 4>{});
-    if (rows <= 32) return fn(Variant<kD, 2, 2>{});
-    if (rows <= 64) return fn(Variant<kD, 4, 1>{});
-    return fn(Variant<kD, 8, 1>{});
+    if constexpr (kD < 64) {
+      if (rows > 64) return fn(Variant<kD, 8, 1>{});
+      if (rows > 32) return fn(Variant<kD, 4, 1>{});
+    }
+    return fn(Variant<kD, 2, 2>{});
   };
   switch (D) {
     case 16: return by_rows(std::integral_constant<int, 16>{});

@@ -18,10 +18,11 @@
 // S has two buffers, so that the next tile's scores are there when a softmax
 // ends.  A softmax is a chain of latencies (scores from TMEM, exponentials,
 // probabilities to TMEM) that grows with the keys a thread takes, and with few
-// rows most lanes would be idle: up to 64 (32) rows are held P = 2 (4) times, in
-// lanes row + 64 (32) i, and copy i takes its share of each tile's keys, with
-// zeros for the others among its probabilities, so the products stay the same
-// instructions.  The copies' maxima, sums and outputs merge at a piece's end.
+// rows most lanes would be idle: up to 64 rows are held P = 2 times, in lanes
+// row + 64 i, and copy i takes its half of each tile's keys, with zeros for the
+// other among its probabilities, so the products stay the same instructions
+// (long trees of 48: 57.3 -> 53.9 us).  The copies' maxima, sums and outputs
+// merge at a piece's end.
 // What a tile holds behind the last key (or the last node) is not the
 // sequence's: its scores are masked, and the row threads clear its value rows
 // before the product.  They also bring the query rows, the next piece's before
@@ -90,12 +91,6 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st8_async(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
-}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -107,9 +102,6 @@ template <typename T>
 __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
-// Tile t of a piece is wholly cached: no key of it is masked.
-__device__ __forceinline__ bool plain(const Piece& p, int t) { return (t + 1) * KT <= p.len; }
-
 template <int D, int P>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -152,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 32) {
     mbar_init(b_q, 1);
-    mbar_init(b_rows, kLanes);
+    mbar_init(b_rows, kLanes / 32);
     for (int s = 0; s < NS; ++s) {
       mbar_init(b_kf(s), 1);
       mbar_init(b_vf(s), 1);
@@ -161,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sf(i), 1);
-      mbar_init(b_pf(i), kLanes);
+      mbar_init(b_pf(i), kLanes / 32);
       mbar_init(b_od(i), 1);
     }
     for (int k = 0; k < kListed; ++k) mbar_init(b_listed(k), 1);
@@ -170,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncwarp();
   if (warp == 1) tmem_alloc(smem_u32(slot), kTmemCols);
-  typename Split<MR, KT>::Pieces pieces{&a, table, 0, 0, 0, 0, 0, 0, 0};
-  if (warp == 0) pieces = Split<MR, KT>::plan(a, table, true);
+  typename Split<MR, KT, 6>::Pieces pieces{&a, table, 0, 0, 0, 0, 0, 0, 0};
+  if (warp == 0) pieces = Split<MR, KT, 6>::plan(a, table, true);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -315,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     // ------------------------------------------------ rows
     constexpr int NC = KT / P;               // keys of a tile that a copy takes
-    constexpr int CW = NC < 32 ? NC : 32;    // ... at a time
     const int e = (warp & 3) * 32 + lane;    // TMEM lane
     const int row = e % MR, copy = e / MR;   // of the tile
     const uint32_t lo = uint32_t((warp & 3) * 32) << 16;
@@ -331,8 +322,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     // barrier of the row threads with a bounded wait: a warp that gave up does
     // not leave the others waiting
     uint32_t syncs = 0;
+    auto arrive = [&](uint32_t bar) {  // once a warp (128 arrivals take their time)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     auto rows_sync = [&] {
-      mbar_arrive(b_rows);
+      arrive(b_rows);
       wait(b_rows, syncs++ & 1, 22);
     };
     // the query rows of a piece (every MMA that read the last piece's is complete:
@@ -418,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!ok) break;
         if (!busy) {
-          mbar_arrive(b_pf(buf_of(g)));
+          arrive(b_pf(buf_of(g)));
           continue;
         }
         tc_fence_after();
@@ -436,33 +431,29 @@ __global__ void __launch_bounds__(kThreads, 2)
         // maximum only when it grows by more than 2^8 (they stay <= 256); 0 is used
         // while the row has seen nothing (every p is then 2^(-inf) = 0).
 #pragma unroll
-        for (int h = 0; h < NC / CW; ++h) {
-          const int key0 = copy * NC + h * CW;
-          float x[CW];
-          if constexpr (CW == 32) {
-            uint32_t r[32];
-            tmem_ld32_async(tSw + key0, r);
-            tmem_wait_ld(r);
+        for (int h = 0; h < NC / 32; ++h) {
+          const int key0 = copy * NC + h * 32;
+          uint32_t r[32];
+          tmem_ld32_async(tSw + key0, r);
+          tmem_wait_ld(r);
+          float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-          } else {
-            tmem_ld16(tSw + key0, x);
-          }
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
           if (!open) {
             const uint32_t bits = uint32_t(see >> key0);
 #pragma unroll
-            for (int i = 0; i < CW; ++i) x[i] = (bits >> i) & 1 ? x[i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) x[i] = (bits >> i) & 1 ? x[i] : -INFINITY;
           }
-          float c2[CW / 16];
+          float c2[2];
 #pragma unroll
-          for (int k2 = 0; k2 < CW / 16; ++k2) {
+          for (int k2 = 0; k2 < 2; ++k2) {
             const float* y = x + 16 * k2;
             float mm = max3f(y[0], y[1], y[2]);
 #pragma unroll
             for (int i = 3; i < 15; i += 2) mm = max3f(mm, y[i], y[i + 1]);
             c2[k2] = fmaxf(mm, y[15]);
           }
-          const float mn = __fmul_rn(fmaxf(c2[0], c2[CW / 16 - 1]), scale);
+          const float mn = __fmul_rn(fmaxf(c2[0], c2[1]), scale);
           const bool resc = mn > m + kRescale;
           if (__any_sync(0xffffffffu, resc)) {
             const float corr = resc ? ex2(m - mn) : 1.f;
@@ -493,10 +484,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-          uint32_t pk[CW / 2];
+          uint32_t pk[16];
           float sa[2] = {0.f, 0.f}, sb[2] = {0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < CW; i += 2) {
+          for (int i = 0; i < 32; i += 2) {
             float u0, u1;
             fma2(u0, u1, x[i], x[i + 1], scale, scale, -base, -base);
             const float p0 = ex2(u0), p1 = ex2(u1);
@@ -509,22 +500,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           if constexpr (P == 1) {
             tmem_st16_async(tSw + 16 * h, pk);
           } else {
-            uint32_t zero[CW / 2];
+            uint32_t zero[16];
 #pragma unroll
-            for (int i = 0; i < CW / 2; ++i) zero[i] = 0;
-#pragma unroll
-            for (int c = 0; c < P; ++c) {
-              const uint32_t at = tSw + ((copy + c) % P) * (CW / 2);
-              if constexpr (P == 2)
-                tmem_st16_async(at, c == 0 ? pk : zero);
-              else
-                tmem_st8_async(at, c == 0 ? pk : zero);
-            }
+            for (int i = 0; i < 16; ++i) zero[i] = 0;
+            tmem_st16_async(tSw + 16 * copy, pk);
+            tmem_st16_async(tSw + 16 * (copy ^ 1), zero);
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(b_pf(buf_of(g)));
+        arrive(b_pf(buf_of(g)));
       }
       if (!ok) break;
       wait(b_listed(k + 1), ((k + 1) / kListed) & 1, 26);
@@ -649,23 +634,16 @@ int launch_tc(const TreeAttnArgs& a, cudaStream_t st) {
   return launch_combine<bf16, F::MR, D>(w, st);
 }
 
-// Copies of a row: as many as fit its tile's 128 lanes.
-int copies(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
+int copies(int rows) { return rows <= 64 ? 2 : 1; }
 
 }  // namespace
 
 size_t tree_attn_tc_workspace(int B, int N, int H, int Hkv, int D) {
-  switch (copies(N * (H / Hkv))) {
-    case 4: return workspace_bytes<32>(grid_size(), B, N, H, Hkv, D);
-    case 2: return workspace_bytes<64>(grid_size(), B, N, H, Hkv, D);
-    default: return workspace_bytes<128>(grid_size(), B, N, H, Hkv, D);
-  }
+  return copies(N * (H / Hkv)) == 2 ? workspace_bytes<64>(grid_size(), B, N, H, Hkv, D)
+                                    : workspace_bytes<128>(grid_size(), B, N, H, Hkv, D);
 }
 
 int launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t st) {
-  switch (copies(a.N * a.G)) {
-    case 4: return a.D == 128 ? launch_tc<128, 4>(a, st) : launch_tc<64, 4>(a, st);
-    case 2: return a.D == 128 ? launch_tc<128, 2>(a, st) : launch_tc<64, 2>(a, st);
-    default: return a.D == 128 ? launch_tc<128, 1>(a, st) : launch_tc<64, 1>(a, st);
-  }
+  if (copies(a.N * a.G) == 2) return a.D == 128 ? launch_tc<128, 2>(a, st) : launch_tc<64, 2>(a, st);
+  return a.D == 128 ? launch_tc<128, 1>(a, st) : launch_tc<64, 1>(a, st);
 }

@@ -9,7 +9,7 @@
 // order, form one list, and every CTA takes an equal run of it, whatever the
 // lengths are: a long sequence is split over many CTAs, short ones share one.
 // Each segment counts kExtra tiles more than it has, for what a piece costs
-// besides its tiles (queries, masks, results).  Lengths are read on the device, so a recorded launch follows
+// besides its tiles (queries, masks, results; each kernel has its own number).  Lengths are read on the device, so a recorded launch follows
 // them.  A segment inside one CTA's run is finished there; the pieces of any
 // other go to the workspace (unnormalised output, running maximum and sum in
 // fp32) and tree_combine_kernel merges them in tile order, so the result does
@@ -44,7 +44,6 @@ __device__ __forceinline__ SeqDims seq_dims(const TreeAttnArgs& a, int b, bool* 
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-constexpr int kExtra = 2;
 constexpr int kTable = 32;  // sequences whose lengths a CTA keeps in shared memory
 
 // One piece of a CTA's run: key tiles [t0, t1) of a segment.
@@ -56,7 +55,7 @@ struct Piece {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == kt; }
 };
 
-template <int MR, int KT>
+template <int MR, int KT, int kExtra>
 struct Split {
   __device__ __forceinline__ static int row_tiles(const TreeAttnArgs& a, SeqDims s) {
     return ceil_div(s.n * a.G, MR);

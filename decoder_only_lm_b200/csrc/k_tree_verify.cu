@@ -48,11 +48,16 @@ constexpr int kIlp = 8;                     // weights of a thread computed toge
 constexpr int kCoarse = 37;          // bins by the exponent of a weight (1 .. 2^36)
 constexpr int kBins = kCoarse * 32;  // ... and the 5 bits behind its leading one
 constexpr int kCand = 48;            // ids of a cut's bin per CTA; more are bisected
+// Weights below 2^kLow are counted in one bin (coarse bin kLow - 1) until a cut
+// falls among them: they are most of a vocabulary and next to nothing of the
+// probability, and a histogram's cost is its atomics (64 sequences with top-k and
+// top-p: 345 -> 2xx us).
+constexpr int kLow = 22;
 constexpr double kOne = 68719476736.0;  // 2^36
 constexpr unsigned kAll = 0xffffffffu;
 
-// A row's cuts.  hist: this CTA's weights (in halves of 18 bits; a slice holds at
-// most 2^13 ids, so 32 bits hold every sum) and ids by bin.
+// A row's cuts: this CTA's weights (in halves of 18 bits; a slice holds at most
+// 2^13 ids, so 32 bits hold every sum) and ids by bin.
 struct Cut {
   uint32_t lo[kBins], hi[kBins], count[kBins];
   // pushed by every CTA: weights and ids by coarse bin
@@ -65,6 +70,8 @@ struct Cut {
   uint64_t key[2][kCluster][kCand], w[2][kCluster][kCand];
   uint32_t n_in[2][kCluster];
   uint32_t n_mine[2];
+  uint16_t mine[kCand];  // this CTA's ids of the bin, before they are pushed
+  bool fine_low;         // the low weights have been sorted into their bins
   int coarse, bin;  // where the cut falls, -1: nowhere
   uint64_t at_n, at_w;  // ids and weight of the bins above it
   double goal;
@@ -73,6 +80,7 @@ struct Cut {
 
 struct Shared {
   uint64_t warp_red[2][2][kWarps];
+  uint32_t warp_n[2][kWarps];
   uint64_t red[2][2][kCluster];  // pushed
   int tok[kTreeMaxNodes], par[kTreeMaxNodes], kid[kTreeMaxNodes];
   float u[kTreeMaxNodes];
@@ -221,7 +229,7 @@ struct Walk {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int k = kCoarse - 1 - 2 * lane - j;
-      if (k >= 0)
+      if (k >= (c.fine_low ? 0 : kLow - 1))
 #pragma unroll
         for (int r = 0; r < kCluster; ++r) {
           un[j] += c.in_n[r][k];
@@ -272,6 +280,54 @@ struct Walk {
     }
   }
 
+  // Sums of the coarse bins [k0, k1) of the histogram pushed to every CTA.
+  __device__ void push_coarse(Cut& c, int k0, int k1) {
+    for (int e = k0 + warp; e < k1; e += kWarps) {
+      const int f = e * 32 + lane;
+      const uint64_t w = warp_add(c.lo[f] + (uint64_t(c.hi[f]) << 18));
+      const uint32_t m = __reduce_add_sync(kAll, c.count[f]);
+      if (lane < kCluster) {
+        *remote(&c.in_w[rank][e], lane) = w;
+        *remote(&c.in_n[rank][e], lane) = m;
+      }
+    }
+  }
+  // The low weights sorted into their bins, of the rows whose cut is among them.
+  template <int K>
+  __device__ void refine(Row (&row)[K], int rows) {
+    bool mine[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      mine[k] = k < rows && !row[k].cut->fine_low && row[k].cut->coarse == kLow - 1;
+    cl.sync();  // every CTA has read the bin that the others' sums replace
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (mine[k]) {
+        Cut& c = *row[k].cut;
+        for (int i = threadIdx.x; i < kLow * 32; i += kThreads) c.lo[i] = c.hi[i] = c.count[i] = 0;
+        if (threadIdx.x == 0) c.fine_low = true;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (mine[k]) {
+        Cut& c = *row[k].cut;
+        for (int i = i0 + lane; i < i1; i += 32) {
+          const uint64_t w = row[k].w[i];
+          if (w == 0 || w >> kLow) continue;
+          const int bin = bin_of(double(w) + kOnes);
+          atomicAdd(&c.lo[bin], uint32_t(w & 0x3FFFF));
+          atomicAdd(&c.hi[bin], uint32_t(w >> 18));
+          atomicAdd(&c.count[bin], 1u);
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (mine[k]) push_coarse(*row[k].cut, 0, kLow);
+    cl.sync();
+  }
+
   // A cut of the rows: the ids before the first at which the running count
   // (by_weight false: to c.goal ids) or weight reaches the goal stay, that one
   // included.  The bin of the place comes from the histograms; its ids are
@@ -283,6 +339,17 @@ struct Walk {
     for (int k = 0; k < K; ++k)
       if (k < rows && warp == k) find_coarse(*row[k].cut, by_weight, share);
     __syncthreads();
+    bool again = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      again |= k < rows && !row[k].cut->fine_low && row[k].cut->coarse == kLow - 1;
+    if (again) {  // the same in every CTA: a cut among the low weights
+      refine(row, rows);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (k < rows && warp == k && row[k].cut->fine_low) find_coarse(*row[k].cut, by_weight, share);
+      __syncthreads();
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k)  // warps 8 k .. 8 k + 7: one CTA's fine bins each
       if (k < rows && warp / kCluster == k && row[k].cut->coarse >= 0) {
@@ -305,6 +372,7 @@ struct Walk {
         }
       }
     __syncthreads();
+    // its ids: first a list of this CTA's, then eight threads an id push them
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (k < rows && row[k].cut->coarse >= 0) {
@@ -314,16 +382,24 @@ struct Walk {
 #pragma unroll 4
         for (int i = i0 + lane; i < i1; i += 32) {
           const uint64_t w = row[k].w[i];
-          if (w < row[k].low || w >= row[k].high) continue;
-          const uint64_t key = order_key(clean(row[k].z[lo + i]), lo + i);
-          if (key < row[k].tau) continue;  // cut away already
-          const uint32_t at = atomicAdd(&c.n_mine[phase], 1u);
-          if (at < kCand)
+          if (w >= row[k].low && w < row[k].high) {
+            const uint32_t at = atomicAdd(&c.n_mine[phase], 1u);
+            if (at < kCand) c.mine[at] = uint16_t(i);
+          }
+        }
+      }
+    __syncthreads();
 #pragma unroll
-            for (int r = 0; r < kCluster; ++r) {
-              *remote(&c.key[phase][rank][at], r) = key;
-              *remote(&c.w[phase][rank][at], r) = w;
-            }
+    for (int k = 0; k < K; ++k)
+      if (k < rows && row[k].cut->coarse >= 0) {
+        Cut& c = *row[k].cut;
+        const int count = min(int(c.n_mine[phase]), kCand);
+        for (int q = threadIdx.x; q < count * kCluster; q += kThreads) {
+          const int at = q / kCluster, r = q % kCluster, i = c.mine[at];
+          const uint64_t key = order_key(clean(row[k].z[lo + i]), lo + i);
+          // (an id that is cut away already counts nothing)
+          *remote(&c.key[phase][rank][at], r) = key < row[k].tau ? 0 : key;
+          *remote(&c.w[phase][rank][at], r) = row[k].w[i];
         }
       }
     __syncthreads();
@@ -350,6 +426,7 @@ struct Walk {
           const int r0 = e % kCluster, j0 = e / kCluster;
           if (j0 >= int(c.n_in[phase][r0])) continue;
           const uint64_t key = c.key[phase][r0][j0];
+          if (key == 0) continue;
           uint64_t ahead = 0;
           for (int q = lane; q < grid; q += 32) {
             const int r = q % kCluster, j = q / kCluster;
@@ -522,19 +599,25 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
     }
     wk.template exchange<K, true>(top);
     // the weights
-    uint64_t sum[K];
+    uint64_t sum[K], low_w[K];
+    uint32_t low_n[K];
     if (kCuts) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        for (int i = tid; i < kBins; i += kThreads)
+        for (int i = kLow * 32 + tid; i < kBins; i += kThreads)
           cut[k].lo[i] = cut[k].hi[i] = cut[k].count[i] = 0;
+      if (tid < K) {
+        cut[tid].fine_low = false;
+        cut[tid].goal = double(top_k);
+      }
       __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       row[k].top = top[k];
       row[k].sum = uint64_t(kOne);  // temperature 0: the highest logit alone
-      sum[k] = 0;
+      sum[k] = low_w[k] = 0;
+      low_n[k] = 0;
       if (k >= rows || T == 0.0) continue;
       const float zmax = key_logit(top[k]), zmin = Exp::floor_of(zmax, a.temperature);
       const bool inf = isinf(zmax);  // the ids at the infinite maximum alone
@@ -558,11 +641,16 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
           if (j0 + j < per && i < wk.i1) {
             row[k].w[i] = w;
             sum[k] += w;
-            if (kCuts && w) {
-              const int bin = bin_of(e[j]);
-              atomicAdd(&cut[k].lo[bin], uint32_t(w & 0x3FFFF));
-              atomicAdd(&cut[k].hi[bin], uint32_t(w >> 18));
-              if (top_k > 0) atomicAdd(&cut[k].count[bin], 1u);
+            if (kCuts) {
+              if (w >> kLow) {
+                const int bin = bin_of(e[j]);
+                atomicAdd(&cut[k].lo[bin], uint32_t(w & 0x3FFFF));
+                atomicAdd(&cut[k].hi[bin], uint32_t(w >> 18));
+                if (top_k > 0) atomicAdd(&cut[k].count[bin], 1u);
+              } else {
+                low_w[k] += w;
+                low_n[k] += w != 0;
+              }
             }
           }
         }
@@ -575,20 +663,28 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
         for (int k = 0; k < K; ++k) row[k].sum = sum[k];
       }
     } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint64_t lw = warp_add(low_w[k]);
+        const uint32_t ln = __reduce_add_sync(kAll, low_n[k]);
+        if (lane == 0) {
+          sh.warp_red[0][k][wk.warp] = lw;
+          sh.warp_n[k][wk.warp] = ln;
+        }
+      }
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (k >= rows) continue;
-        for (int e = wk.warp; e < kCoarse; e += kWarps) {
-          const int f = e * 32 + lane;
-          const uint64_t w = warp_add(cut[k].lo[f] + (uint64_t(cut[k].hi[f]) << 18));
-          const uint32_t m = __reduce_add_sync(kAll, cut[k].count[f]);
+        wk.push_coarse(cut[k], kLow, kCoarse);
+        if (wk.warp == kWarps - 1 - k) {
+          const uint64_t lw = warp_add(lane < kWarps ? sh.warp_red[0][k][lane] : 0);
+          const uint32_t ln = __reduce_add_sync(kAll, lane < kWarps ? sh.warp_n[k][lane] : 0u);
           if (lane < kCluster) {
-            *wk.remote(&cut[k].in_w[rank][e], lane) = w;
-            *wk.remote(&cut[k].in_n[rank][e], lane) = m;
+            *wk.remote(&cut[k].in_w[rank][kLow - 1], lane) = lw;
+            *wk.remote(&cut[k].in_n[rank][kLow - 1], lane) = ln;
           }
         }
-        if (tid == 0) cut[k].goal = double(top_k);
       }
       cl.sync();
       if (top_k > 0) {

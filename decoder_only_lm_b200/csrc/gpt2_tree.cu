@@ -78,7 +78,7 @@ int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits,
   if (B < 1 || B > 65535 || N < 1 || N > kTreeMaxNodes || V < 1 || V > kTreeMaxVocab || ld < V ||
       (draft_logits && ld_draft < V))
     return refuse("tree_verify: B, N (1..256), V (1..65536) or a row stride out of range");
-  if (!(temperature >= 0.f && temperature <= 1e30f) || top_k < 0 ||
+  if (!(temperature >= 0.f && temperature <= 1e20f) || top_k < 0 ||
       !(top_p > 0.f && top_p <= 1.f))
     return refuse("tree_verify: bad sampling settings");
   try {

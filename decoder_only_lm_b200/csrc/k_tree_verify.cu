@@ -33,28 +33,22 @@
 #include <cooperative_groups.h>
 
 #include "kernels.h"
-#include "tree_internal.h"
+#include "tree_verify.cuh"
 
 namespace cg = cooperative_groups;
+using namespace tree;
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-constexpr int kMaxSlice = kTreeMaxVocab / kCluster;
-constexpr int kPer = kMaxSlice / kThreads;  // ids of a thread at most
-constexpr int kIlp = 8;                     // weights of a thread computed together
+constexpr int kIlp = 8;              // weights of a thread computed together
 constexpr int kCoarse = 37;          // bins by the exponent of a weight (1 .. 2^36)
 constexpr int kBins = kCoarse * 32;  // ... and the 5 bits behind its leading one
 constexpr int kCand = 48;            // ids of a cut's bin per CTA; more are bisected
 // Weights below 2^kLow are counted in one bin (coarse bin kLow - 1) until a cut
 // falls among them: they are most of a vocabulary and next to nothing of the
-// probability, and a histogram's cost is its atomics (64 sequences with top-k and
-// top-p: 345 -> 2xx us).
+// probability, and a histogram's cost is its atomics (16 trees of 64, 50257 ids,
+// top-p: 37.4 -> 35.9 us).
 constexpr int kLow = 22;
-constexpr double kOne = 68719476736.0;  // 2^36
-constexpr unsigned kAll = 0xffffffffu;
 
 // A row's cuts: this CTA's weights (in halves of 18 bits; a slice holds at most
 // 2^13 ids, so 32 bits hold every sum) and ids by bin.
@@ -78,61 +72,11 @@ struct Cut {
   uint64_t tau, kept;  // lowest ordering key that stays, weight that stays
 };
 
-struct Shared {
+struct Shared : Tree {
   uint64_t warp_red[2][2][kWarps];
   uint32_t warp_n[2][kWarps];
   uint64_t red[2][2][kCluster];  // pushed
-  int tok[kTreeMaxNodes], par[kTreeMaxNodes], kid[kTreeMaxNodes];
-  float u[kTreeMaxNodes];
-  uint64_t kw[kTreeMaxNodes], kx[kTreeMaxNodes];
-  double exp_table[64];
-  int n_kids;
 };
-
-// Order of the ids of a row: by logit, the smaller id first among equal ones.
-__device__ __forceinline__ uint32_t order_of(float z) {
-  const uint32_t b = __float_as_uint(z + 0.f);  // -0 counts as 0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ uint64_t order_key(float z, int id) {
-  return (uint64_t(order_of(z)) << 32) | uint64_t(0xFFFFFFFFu - uint32_t(id));
-}
-__device__ __forceinline__ float key_logit(uint64_t key) {
-  const uint32_t ord = uint32_t(key >> 32);
-  return __uint_as_float((ord & 0x80000000u) ? (ord & 0x7FFFFFFFu) : ~ord);
-}
-__device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z; }
-
-// rint(2^36 exp(-d / T)) for d = zmax - z >= 0 (zmax finite).  With x = 64 d
-// log2(e) / T = r - n, n the nearest integer (from the 1.5 * 2^52 shift):
-// 2^36 exp(-d / T) = 2^(36 + n / 64) 2^(r / 64), the first factor from a table of
-// 64 and an exponent, the second from its Taylor sum, |r ln2 / 64| < 0.0055: the
-// first term left out is below 4e-17.  A weight is within 2^-14 of the value it
-// rounds.  Returned as 2^52 + weight, whose low 52 bits are the integer.
-constexpr double kOnes = 4503599627370496.0;  // 2^52
-struct Exp {
-  const double* table;  // 2^(36 + i / 64)
-  double per_unit;      // -64 log2(e) / T
-  // logits below it have weight 0: 2^36 exp(-40) < 1/2 (NaN and -inf with them)
-  __device__ static float floor_of(float zmax, float T) { return fmaxf(zmax - 40.f * T, -3e38f); }
-  __device__ double operator()(float z, float zmax, float zmin) const {
-    constexpr double kShift = 6755399441055744.0;  // 1.5 * 2^52
-    constexpr double c = 0.010830424696249145;     // ln(2) / 64
-    const double d = double(zmax) - double(fmaxf(z, zmin));
-    const double t = fma(d, per_unit, kShift);
-    const double r = fma(d, per_unit, kShift - t);
-    const int n = __double2loint(t);
-    double p = fma(r, c * c * c * c * c / 120, c * c * c * c / 24);
-    p = fma(r, p, c * c * c / 6);
-    p = fma(r, p, c * c / 2);
-    p = fma(r, p, c);
-    p = fma(r, p, 1.0) * table[n & 63];
-    return __hiloint2double(__double2hiint(p) + ((n & ~63) << 14), __double2loint(p)) + kOnes;
-  }
-};
-__device__ __forceinline__ uint64_t integer_of(double v) {
-  return uint64_t(__double_as_longlong(v)) & 0xFFFFFFFFFFFFFull;
-}
 
 // Bin of a weight >= 1 (as 2^52 + weight): its exponent and the 5 bits behind
 // the leading one; the bin's weights are [bin_low(bin), bin_low(bin + 1)).
@@ -142,29 +86,6 @@ __device__ __forceinline__ int bin_of(double v) {
 __device__ __forceinline__ uint64_t bin_low(int bin) {
   const uint64_t m = uint64_t(32 + (bin & 31)) << (bin >> 5);
   return (m + 31) >> 5;  // small exponents have fewer than 32 weights
-}
-
-// Sum over a warp of values below 2^53: three parts of 21 bits, 32 of which fit
-// 32 bits.
-__device__ __forceinline__ uint64_t warp_add(uint64_t v) {
-  const uint64_t a = __reduce_add_sync(kAll, uint32_t(v) & 0x1FFFFFu);
-  const uint64_t b = __reduce_add_sync(kAll, uint32_t(v >> 21) & 0x1FFFFFu);
-  const uint64_t c = __reduce_add_sync(kAll, uint32_t(v >> 42));
-  return a + (b << 21) + (c << 42);
-}
-__device__ __forceinline__ uint64_t warp_top(uint64_t v) {
-  const uint32_t hi = __reduce_max_sync(kAll, uint32_t(v >> 32));
-  const uint32_t lo = __reduce_max_sync(kAll, uint32_t(v >> 32) == hi ? uint32_t(v) : 0u);
-  return (uint64_t(hi) << 32) | lo;
-}
-// Inclusive running sum over a warp's lanes.
-__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(kAll, v, o);
-    if (lane >= o) v += y;
-  }
-  return v;
 }
 
 struct Row {
@@ -508,31 +429,11 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
   const double T = double(a.temperature), top_p = double(a.top_p);
   const int top_k = a.top_k < a.V ? a.top_k : 0;
   Cut* cut = reinterpret_cast<Cut*>(dyn + slice * K);
-  const float* u = a.uniform + int64_t(b) * a.N;
   int32_t* path = a.path + int64_t(b) * a.N;
-  auto unit = [](float v) { return double(fminf(fmaxf(v, 0.f), 1.f)); };
 
-  int N = a.counts ? a.counts[b] : a.N;
-  bool bad = N < 0 || N > a.N;
-  if (bad) N = 0;
-  for (int i = tid; i < a.N; i += kThreads) {
-    if (rank == 0) path[i] = i == 0 && N > 0 ? 0 : -1;
-    sh.tok[i] = a.tokens[int64_t(b) * a.N + i];
-    sh.u[i] = u[i];
-    const int p = a.parent ? a.parent[int64_t(b) * a.N + i] : i - 1;
-    if (i < N && (p < -1 || p >= i)) bad = true;
-    sh.par[i] = p;
-  }
-  if (bad && rank == 0) atomicExch(a.err, kTreeBadInput);
-  if (tid < 64) sh.exp_table[tid] = exp2(36.0 + tid / 64.0);
-  const Exp ex{sh.exp_table, -64.0 * 1.4426950408889634 / T};
-  if (N == 0) {  // the whole cluster
-    if (rank == 0 && tid == 0) {
-      a.n_path[b] = 0;
-      a.next[b] = -1;
-    }
-    return;
-  }
+  const int N = load_tree(a, sh, b, rank, tid);
+  const Exp ex(sh.exp_table, a.temperature);
+  if (N == 0) return;  // the whole cluster
   cl.sync();  // every CTA has started: the others may write into its shared memory
 
   int cur = 0, n_path = 1;
@@ -556,18 +457,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
       }
     };
     fetch(0);
-    // children of cur, in id order
-    if (wk.warp == 0) {
-      int m = 0;
-      for (int j0 = cur + 1; j0 < N; j0 += 32) {
-        const int j = j0 + lane;
-        const bool is = j < N && sh.par[j] == cur;
-        const unsigned which = __ballot_sync(kAll, is);
-        if (is) sh.kid[m + __popc(which & ((1u << lane) - 1))] = j;
-        m += __popc(which);
-      }
-      if (lane == 0) sh.n_kids = m;
-    }
+    if (wk.warp == 0) find_children(sh, cur, N, lane);
     __syncthreads();
     const int n_kids = sh.n_kids;
     const int rows = K == 2 && n_kids > 0 ? 2 : 1;
@@ -619,8 +509,13 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
       sum[k] = low_w[k] = 0;
       low_n[k] = 0;
       if (k >= rows || T == 0.0) continue;
-      const float zmax = key_logit(top[k]), zmin = Exp::floor_of(zmax, a.temperature);
-      const bool inf = isinf(zmax);  // the ids at the infinite maximum alone
+      float zmax = key_logit(top[k]);
+      if (ex.lone(zmax)) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[k][j] = only(v[k][j], zmax);
+        zmax = 0.f;
+      }
+      const float zmin = ex.lowest(zmax);
       // kIlp at a time with no branch between them: the chains of dependent fp64
       // operations overlap
 #pragma unroll
@@ -629,11 +524,6 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
         double e[kIlp];
 #pragma unroll
         for (int j = 0; j < kIlp; ++j) e[j] = ex(v[k][j0 + j], zmax, zmin);
-        if (inf) {
-#pragma unroll
-          for (int j = 0; j < kIlp; ++j)
-            e[j] = clean(v[k][j0 + j]) == zmax ? kOnes + kOne : kOnes;
-        }
 #pragma unroll
         for (int j = 0; j < kIlp; ++j) {
           const int i = wk.i0 + 32 * (j0 + j) + lane;
@@ -704,15 +594,12 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const uint64_t key = order_key(kid_z[k], kid_tok);
-        const float zmax = key_logit(row[k].top), zmin = Exp::floor_of(zmax, a.temperature);
         if (!kid_real || k >= rows)
           kid_w[k] = 0;
         else if (T == 0.0)
           kid_w[k] = key == row[k].top ? uint64_t(kOne) : 0;
-        else if (isinf(zmax))
-          kid_w[k] = kid_z[k] == zmax && key >= row[k].tau ? uint64_t(kOne) : 0;
         else
-          kid_w[k] = key < row[k].tau ? 0 : integer_of(ex(kid_z[k], zmax, zmin));
+          kid_w[k] = key < row[k].tau ? 0 : weight_of(ex, kid_z[k], key_logit(row[k].top));
       }
       sh.kw[tid] = kid_w[0];
       sh.kx[tid] = kid_w[K - 1];
@@ -736,10 +623,6 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
       }
       if (T == 0.0) continue;  // the one weight stays: it is accepted or not proposed
       if (kDraft) {
-        auto less = [f](uint64_t wi, uint64_t xi) {
-          const int64_t r = int64_t(wi) - __double2ll_rn(double(xi) * f);
-          return r > 0 ? uint64_t(r) : uint64_t(0);
-        };
         if (!trimmed) {
           wk.trim(row[0]);
           wk.trim(row[K - 1]);
@@ -752,7 +635,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
 #pragma unroll
           for (int q = j1; q < j1 + 4; ++q) {
             const int i = wk.i0 + 32 * q + lane;
-            wi[q] = q < per && i < wk.i1 ? less(w[i], x[i]) : 0;
+            wi[q] = q < per && i < wk.i1 ? less(w[i], x[i], f) : 0;
             left[0] += wi[q];
           }
         }
@@ -764,7 +647,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
             const int i = wk.i0 + 32 * q + lane;
             if (q < per && i < wk.i1) w[i] = wi[q];
           }
-          for (int i = tid; i < n_kids; i += kThreads) sh.kw[i] = less(sh.kw[i], sh.kx[i]);
+          for (int i = tid; i < n_kids; i += kThreads) sh.kw[i] = less(sh.kw[i], sh.kx[i], f);
         }
       } else if (wc && S > wc) {
         const int t = sh.tok[c];
@@ -871,7 +754,11 @@ int launch(const TreeVerifyArgs& a, cudaStream_t st) {
 }  // namespace
 
 int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st) {
-  const bool cuts = a.temperature > 0.f && ((a.top_k > 0 && a.top_k < a.V) || a.top_p < 1.f);
+  const bool top = a.temperature > 0.f && a.top_k > 0 && a.top_k < a.V;
+  // the kept ids as a list, as long as they fit (3 to 4 times as fast as the
+  // histogram wherever both were measured: its figures stand with it)
+  if (top && a.top_k <= kTreeTop) return launch_tree_verify_top(a, st);
+  const bool cuts = top || (a.temperature > 0.f && a.top_p < 1.f);
   if (a.draft) return cuts ? launch<true, true>(a, st) : launch<true, false>(a, st);
   return cuts ? launch<false, true>(a, st) : launch<false, false>(a, st);
 }

@@ -44,6 +44,9 @@ struct TreeVerifyArgs {
 constexpr int kTreeMaxNodes = 256;
 constexpr int kTreeMaxVocab = 65536;
 int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st);
+// the same for a temperature above 0 and 1 <= top_k <= kTreeTop, top_k < V
+constexpr int kTreeTop = 256;
+int launch_tree_verify_top(const TreeVerifyArgs& a, cudaStream_t st);
 
 struct KvAppendArgs {
   const void* qkv;

@@ -593,7 +593,7 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
  * A token outside [0, V) is never accepted.  A node with parent -1 other than
  * the root is never reached.  All integers exact and deterministic.
  * GPT2_ERR_ARG unless 1 <= V <= 65536, V <= ld (and ld_draft), 0 <= temperature
- * <= 1e30, top_k >= 0, 0 < top_p <= 1, 1 <= N <= 256. */
+ * <= 1e20, top_k >= 0, 0 < top_p <= 1, 1 <= N <= 256. */
 int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits, int64_t ld_draft,
                      const int32_t* tokens, const int32_t* parent, const int32_t* counts,
                      const float* uniform, int B, int N, int V, float temperature, int top_k,

@@ -371,6 +371,50 @@ def test_verify_special_rows(g, draft, setting):
     assert g.device_error() == 0
 
 
+@pytest.mark.parametrize("draft", [False, True], ids=["guess", "draft"])
+@pytest.mark.parametrize("k,p", [(0, 1.0), (0, 0.9), (40, 0.9)])
+@pytest.mark.parametrize("T", [1e-30, 1e-7, 0.8, 1e20])
+def test_verify_extreme_logits(g, draft, k, p, T):
+    """Logits whose fp32 steps are coarser than the temperature, rows masked with
+    the type's lowest value, temperatures at the ends of their range."""
+    B, N, V = 8, 6, 1500
+    z, y, tok, par, u = make_verify(13, B, N, V, True, scale=2.0)
+    low = np.finfo(np.float32).min
+    z[0] = low
+    z[1, :, 9:] = low
+    z[2] = low
+    z[2, :, ::3] = -np.inf
+    z[3] *= np.float32(1e9)
+    z[4] += np.float32(1e6)
+    z[5] = np.where(z[5] > 1, np.float32(3.3e38), np.float32(-3.3e38))
+    z[6] *= np.float32(1e-38)
+    y[:4], y[5] = z[:4], z[5]
+    par[:, 1:4] = 0
+    check_verify(g, z, tok, par, u, T, k, p, draft=y if draft else None)
+    assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("draft", [False, True], ids=["guess", "draft"])
+@pytest.mark.parametrize("V,k,p", [(2, 1, 1.0), (300, 256, 0.9), (257, 256, 1.0), (300, 257, 0.9),
+                                   (5000, 1, 0.5), (5000, 255, 1.0), (5000, 256, 0.7),
+                                   (5000, 257, 0.7), (65536, 200, 0.95)])
+def test_verify_top_k(g, draft, V, k, p):
+    """Kept lists of all lengths: the best ids in one place, equal logits across
+    the cut (in few places and in many), and fewer ids that have a weight."""
+    B, N = 7, 5
+    z, y, tok, par, u = make_verify(V + k, B, N, V, True, scale=3.0)
+    z[1] = -np.sort(-z[1], -1)                       # the first ids
+    z[2] = np.round(z[2])                            # hundreds of equal ones
+    z[3, :, ::2] = z[3].max(-1, keepdims=True)       # half of them equal and best
+    z[4, :, 60:] = -np.inf
+    z[5, :, :V - V // 9] = -3e38                     # a mask of low values
+    y[1], y[3] = -np.sort(-y[1], -1), 0.0
+    y[6] = z[6]
+    par[:, 1:4] = 0
+    check_verify(g, z, tok, par, u, 0.9, k, p, draft=y if draft else None, pad=3)
+    assert g.device_error() == 0
+
+
 def test_verify_bad_counts_and_parents(g):
     z, y, tok, par, u = make_verify(2, 3, 6, 100, False)
     import torch

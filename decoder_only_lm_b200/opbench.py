@@ -8,6 +8,9 @@
     python -m decoder_only_lm_b200.opbench layer_gemms --M 16384 --C 768 (one block's linear layers)
     python -m decoder_only_lm_b200.opbench sample --B 16 --V 50257 [--temperature 0.8 --top-k 0 --top-p 0.9]
     python -m decoder_only_lm_b200.opbench generate --B 16 --T0 64 --new 64 [--cached] (GPT-2 124M, bf16)
+    python -m decoder_only_lm_b200.opbench tree_attention --B 16 --nodes 64 --T 2048 --C 768 --H 12 [--kv-heads 12]
+    python -m decoder_only_lm_b200.opbench tree_verify --B 64 --nodes 12 --V 50257 [--draft --top-k 200]
+    python -m decoder_only_lm_b200.opbench kv_append --B 16 --nodes 64 --layers 24 --C 1024 --H 16
 
 Each call is timed with CUDA events on the current stream after warm-up and
 reported as one JSON line (ms per call, and TFLOP/s or GB/s of algorithmic
@@ -61,10 +64,19 @@ EPIS = {"bias": g.LINEAR_BIAS, "gelu": g.LINEAR_BIAS_GELU, "resid": g.LINEAR_RES
         "gelu_bwd": g.LINEAR_GELU_BWD}
 
 
+def random_trees(B, N, dev):
+    """parent [B, N] int32: node 0 follows the cache, the others one of the four
+    nodes before them."""
+    i = torch.arange(N, device=dev)
+    back = 1 + torch.randint(0, 4, (B, N), device=dev)
+    return torch.where(i > 0, (i - back).clamp(min=0), i - 1).int().contiguous()
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("op", choices=["matmul", "lmhead", "attention", "layernorm", "linear",
-                                   "sample", "generate", "layer_gemms"])
+                                   "sample", "generate", "layer_gemms", "tree_attention",
+                                   "tree_verify", "kv_append"])
     ap.add_argument("--temperature", type=float, default=0.8)
     ap.add_argument("--top-k", type=int, default=0)
     ap.add_argument("--top-p", type=float, default=0.9)
@@ -83,6 +95,10 @@ def main():
     ap.add_argument("--B", type=int, default=16)
     ap.add_argument("--T", type=int, default=1024)
     ap.add_argument("--H", type=int, default=12)
+    ap.add_argument("--nodes", type=int, default=64, help="drafted nodes of a sequence")
+    ap.add_argument("--kv-heads", type=int, default=0, help="heads of the cache (0: as many as H)")
+    ap.add_argument("--layers", type=int, default=12)
+    ap.add_argument("--draft", action="store_true", help="verify against the draft's rows")
     ap.add_argument("--a-mn", action="store_true")
     ap.add_argument("--b-mn", action="store_true")
     ap.add_argument("--accumulate", action="store_true")
@@ -192,6 +208,43 @@ def main():
                    top_p=a.top_p, ms=ms, ms_per_token_step=ms / a.new,
                    tokens_per_s=a.B * a.new / ms * 1e3)
         m.close()
+    elif a.op == "tree_attention":
+        # every sequence T cached positions and a tree of `nodes` nodes
+        Hkv, D, N = a.kv_heads or a.H, a.C // a.H, a.nodes
+        kc, vc = (torch.randn((a.B, Hkv, a.T, D), device=dev).bfloat16() for _ in range(2))
+        qkv = torch.randn((a.B, N, (a.H + 2 * Hkv) * D), device=dev).bfloat16()
+        lens = torch.full((a.B,), a.T, dtype=torch.int32, device=dev)
+        par = random_trees(a.B, N, dev)
+        fn = lambda: g.tree_attention(qkv, kc, vc, lens, a.H, parent=par)
+        ms = timed(fn, a.iters, a.warmup)
+        by = 2.0 * (2 * kc.numel() + qkv.numel() + a.B * N * a.H * D)
+        out.update(B=a.B, nodes=N, T=a.T, C=a.C, H=a.H, kv_heads=Hkv, ms=ms, gbs=by / ms / 1e6,
+                   tflops_algorithmic=4.0 * a.B * N * a.H * D * a.T / ms / 1e9)
+    elif a.op == "tree_verify":
+        # drafted tokens taken from the draft's (or the target's) own rows
+        N = a.nodes
+        z = 4.0 * torch.randn((a.B, N, a.V), device=dev)
+        y = z + torch.randn_like(z) if a.draft else None
+        par = random_trees(a.B, N, dev)
+        rows = torch.softmax(z if y is None else y, -1)
+        tok = torch.multinomial(rows.view(-1, a.V), 1).view(a.B, N)
+        tok = tok.gather(1, par.clamp(min=0).long()).int()
+        u = torch.rand((a.B, N), device=dev)
+        fn = lambda: g.tree_verify(z, a.V, tok, u, a.temperature, a.top_k, a.top_p, parent=par,
+                                   draft_logits=y)
+        ms = timed(fn, a.iters, a.warmup)
+        out.update(B=a.B, nodes=N, V=a.V, draft=a.draft, temperature=a.temperature, top_k=a.top_k,
+                   top_p=a.top_p, ms=ms, nodes_kept=float(fn()[1].float().mean()))
+    elif a.op == "kv_append":
+        Hkv, D, N, L = a.kv_heads or a.H, a.C // a.H, a.nodes, a.layers
+        kc, vc = (torch.zeros((L, a.B, Hkv, a.T, D), device=dev, dtype=torch.bfloat16)
+                  for _ in range(2))
+        qkv = torch.randn((L, a.B, N, (a.H + 2 * Hkv) * D), device=dev).bfloat16()
+        lens = torch.full((a.B,), a.T - N, dtype=torch.int32, device=dev)
+        fn = lambda: g.kv_append(qkv, kc, vc, lens)
+        ms = timed(fn, a.iters, a.warmup)
+        by = 2.0 * 2 * 2 * L * a.B * N * Hkv * D
+        out.update(B=a.B, nodes=N, layers=L, C=a.C, H=a.H, kv_heads=Hkv, ms=ms, gbs=by / ms / 1e6)
     elif a.op == "lmhead":
         h = torch.randn((a.M, a.C), device=dev).bfloat16()
         W = (0.02 * torch.randn((a.Vp, a.C), device=dev)).bfloat16()

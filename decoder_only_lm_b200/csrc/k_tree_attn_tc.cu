@@ -58,7 +58,8 @@ struct Cfg {
   static constexpr int kNodes = P > 1 ? MR : kMaxNodes;   // a node has a row at least
   static constexpr int kMasks = kNodes * (kMaskWords + 1) * 4;
   static constexpr int LX = 20;                  // row stride of the copies' exchange
-  static constexpr int kExchange = P > 1 ? kLanes * (LX + 2) * 4 : 0;
+  static constexpr int kXch = D == 64 ? 2 : 1;   // ... and its buffers
+  static constexpr int kExchange = P > 1 ? kLanes * (kXch * LX + 2) * 4 : 0;
   static constexpr int kSmem = kQ + NS * 2 * kTile + kMasks + kExchange + 1280 + 1024;
 };
 
@@ -91,6 +92,12 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// 16 bytes to shared memory, zeros where the row is not real
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -117,10 +124,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t* mask = reinterpret_cast<uint32_t*>(ring + NS * 2 * F::kTile);
   int* up = reinterpret_cast<int*>(mask + F::kNodes * kMaskWords);
   float* xch = reinterpret_cast<float*>(up + F::kNodes);  // 16 outputs a lane, for the other copies
-  float2* ml = reinterpret_cast<float2*>(xch + kLanes * F::LX);  // ... maximum and sum
+  float2* ml = reinterpret_cast<float2*>(xch + kLanes * F::LX * F::kXch);  // ... maximum and sum
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(up + F::kNodes) + F::kExchange);
   // k_full[NS] | v_full[NS] | k_empty[NS] | v_empty[NS] | q_full | s_full[2] | p_full[2] |
-  // o_done[2] | rows | listed[kListed]
+  // o_done[2] | rows | listed[kListed] | go
   auto b_kf = [&](int s) { return smem_u32(bars + s); };
   auto b_vf = [&](int s) { return smem_u32(bars + NS + s); };
   auto b_ke = [&](int s) { return smem_u32(bars + 2 * NS + s); };
@@ -131,7 +138,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto b_od = [&](int i) { return smem_u32(bars + 4 * NS + 5 + i); };
   const uint32_t b_rows = smem_u32(bars + 4 * NS + 7);
   auto b_listed = [&](int k) { return smem_u32(bars + 4 * NS + 8 + k % kListed); };
-  Listed* list = reinterpret_cast<Listed*>(bars + 4 * NS + 8 + kListed);
+  const uint32_t b_go = smem_u32(bars + 4 * NS + 8 + kListed);
+  Listed* list = reinterpret_cast<Listed*>(bars + 4 * NS + 9 + kListed);
   uint64_t* bad = reinterpret_cast<uint64_t*>(list + kListed);  // nodes of non-finite values
   uint32_t* flag = reinterpret_cast<uint32_t*>(bad + kMaxNodes / 64);
   uint32_t* slot = flag + 1;
@@ -145,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 32) {
     mbar_init(b_q, 1);
     mbar_init(b_rows, kLanes / 32);
+    mbar_init(b_go, kLanes / 32);
     for (int s = 0; s < NS; ++s) {
       mbar_init(b_kf(s), 1);
       mbar_init(b_vf(s), 1);
@@ -190,6 +199,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         static_cast<Piece&>(p) = q;
         mbar_arrive(b_listed(k));
         if (q.kt == 0) break;
+        // the first queries are asked for ahead of a ring of tiles, behind which
+        // they would queue (from cold caches, 16 trees of 64 39 -> 37 us, 8 trees of
+        // 64 with 4 query heads for a cache head 84 -> 80)
+        if (k == 0 && !mbar_wait(b_go, 0, a.err, 27)) {
+          ok = false;
+          break;
+        }
         const int row0 = (q.b * a.Hkv + q.hk) * a.Tc;  // rows of the caches fit 31 bits
         for (int t = q.t0; t < q.t1; ++t) {
           const bool fresh = t >= q.ct;
@@ -330,22 +346,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       arrive(b_rows);
       wait(b_rows, syncs++ & 1, 22);
     };
-    // the query rows of a piece (every MMA that read the last piece's is complete:
-    // its scores have been taken)
-    auto load_q = [&](const Piece& q) {
+    // The query rows of a piece, on their way as soon as the last piece's last
+    // scores are there (every MMA that read its rows is complete then) ...
+    auto start_q = [&](const Piece& q) {
       const bool real = row < q.rows;
       const int gr = q.rt * MR + (real ? row : 0), node = gr / a.G, h = q.hk * a.G + gr % a.G;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          qkv + (int64_t(q.b) * a.N + node) * a.ld_qkv + int64_t(h) * D);
+      const bf16* src = qkv + (int64_t(q.b) * a.N + node) * a.ld_qkv + int64_t(h) * D;
 #pragma unroll
-      for (int c0 = 0; c0 < D / 8; c0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = real ? src[c0 + c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(smem + (c0 >> 3) * F::kChunkQ + e * 128 + ((c ^ (e & 7)) << 4)) = v[c];
-      }
+      for (int c = 0; c < D / 8; ++c)
+        cp_async16(sQ + (c >> 3) * F::kChunkQ + e * 128 + (((c & 7) ^ (e & 7)) << 4), src + c * 8, real);
+    };
+    // ... and theirs to multiply.
+    auto finish_q = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async();  // visible to the MMAs
       rows_sync();
       if (e == 0) mbar_arrive(b_q);
@@ -384,7 +397,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       return found;
     };
     wait(b_listed(0), 0, 26);
-    if (ok && list[0].kt > 0) load_q(list[0]);
+    if (ok && list[0].kt > 0) {
+      start_q(list[0]);
+      arrive(b_go);
+      const Piece& q = list[0];
+      if (a.parent && q.t1 > q.ct) {  // meanwhile its sequence's masks
+        Parents parents;
+        parents.load(a.parent + int64_t(q.b) * a.N, q.n, e, kLanes);
+        build_masks(parents, q.n, mask, up, flag, a.err, e, kLanes, rows_sync);
+        mask_of = q.b;
+      }
+      finish_q();
+    }
     for (int k = 0; ok; ++k) {
       const Listed& p = list[k % kListed];
       if (p.kt == 0) break;
@@ -399,6 +423,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       float m = -INFINITY, l = 0.f;
       for (int t = p.t0; t < t1; ++t, ++g, first = false) {
         wait(b_sf(buf_of(g)), par_of(g), 14);
+        if (t == t1 - 1) {  // (the plan does not wait for this tile)
+          wait(b_listed(k + 1), ((k + 1) / kListed) & 1, 26);
+          if (ok && list[(k + 1) % kListed].kt > 0) start_q(list[(k + 1) % kListed]);
+        }
         if ((t + 1) * KT > len) {
           if (t == max(p.t0, ct)) {  // the piece's first node tile
             rows_sync();             // (the last piece's words and masks have been read)
@@ -512,10 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         arrive(b_pf(buf_of(g)));
       }
       if (!ok) break;
-      wait(b_listed(k + 1), ((k + 1) / kListed) & 1, 26);
-      if (!ok) break;
-      if (list[(k + 1) % kListed].kt > 0)
-        load_q(list[(k + 1) % kListed]);  // the next piece's scores overlap this one's results
+      if (list[(k + 1) % kListed].kt > 0) finish_q();  // its scores overlap this one's results
       wait(b_od(buf_of(g - 1)), par_of(g - 1), 19);
       if (!ok) break;
       tc_fence_after();
@@ -547,18 +572,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < 16; ++i) x[i] *= f;
         }
         if constexpr (P > 1) {
-          // 16 columns at a time; the copies finish them in turn
+          // 16 columns at a time; the copies finish them in turn.  (With two buffers
+          // the next exchange's barrier tells that this one has been read.)
+          float* xc = xch + (c / 16) % F::kXch * (kLanes * F::LX);
           if (busy) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(xch + e * F::LX + i) =
+              *reinterpret_cast<float4*>(xc + e * F::LX + i) =
                   make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
           }
           rows_sync();
           if (busy && copy == (c / 16) % P) {
 #pragma unroll
             for (int k2 = 1; k2 < P; ++k2) {
-              const float* y = xch + (row + (copy + k2) % P * MR) * F::LX;
+              const float* y = xc + (row + (copy + k2) % P * MR) * F::LX;
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
                 const float4 v = *reinterpret_cast<const float4*>(y + i);
@@ -569,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
             }
           }
-          rows_sync();
+          if (F::kXch == 1) rows_sync();
         }
         if (!real || copy != (c / 16) % P) continue;
         if (whole) {

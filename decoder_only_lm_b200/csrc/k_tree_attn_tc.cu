@@ -30,6 +30,12 @@
 // With two CTAs' shared memory little is left for the L1 cache, so nothing in
 // the steps may live in local memory (a spilled register costs an L2 access).
 //
+// What bounds it: with few rows a head the cache's bytes (B200, 4 trees of 48 over
+// 9-33 thousand positions, 12 heads of 64: 52 us, 4.9 TB/s), with full tiles the
+// softmax (8 trees of 64 over 1000-8191, 32 heads on 8 of 128: 65 us), and in short
+// calls the start, a piece's end and the merge (16 trees of 64 over 100-1024, 16
+// heads of 64: 27 us).
+//
 // Every wait is bounded (2 s) and reports a timeout in the error word.
 
 #include "tc_common.cuh"

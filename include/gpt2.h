@@ -555,7 +555,7 @@ int gpt2_linear(int epi, const void* x, const void* w, int w_kn, const float* bi
  * to lens[b] and not written; what other nodes or cache rows hold (infinities
  * and NaN too) does not reach a row.  Rows of nodes i >= counts[b] of out and
  * lse are left as they were.  out: row (b, i) at (b N + i) ld_out, ld_out >=
- * H D.  fp32 accumulation and softmax; with GPT2_BF16 the probabilities are
+ * H D; out, lse and workspace overlap nothing else.  fp32 accumulation and softmax; with GPT2_BF16 the probabilities are
  * rounded to bf16 for the product with v.  workspace: device memory of at least
  * gpt2_tree_attention_workspace() bytes, free again when the call's work is
  * done (calls that may overlap need one each).  Results do not depend on
@@ -605,7 +605,7 @@ int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits,
  * becomes the k, v part of row path[b N + r] of qkv ([n_layer, B, N] rows,
  * ld_qkv apart).  path NULL: rows 0, 1, ...; n_path NULL: N each.
  * new_lens[b] (nullable, not lens itself) = lens[b] + n_path[b].  Nothing else
- * of the caches is touched.  A sequence whose rows would not fit (lens[b] < 0,
+ * of the caches is touched; they do not overlap qkv.  A sequence whose rows would not fit (lens[b] < 0,
  * n_path[b] outside 0 .. N, or lens[b] + n_path[b] > Tc) is left as it is, its
  * new_lens[b] = lens[b]; a node index outside [0, N) is skipped; both are
  * recorded for gpt2_device_error (GPT2_ERR_ARG). */

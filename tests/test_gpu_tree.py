@@ -342,7 +342,8 @@ def test_verify_chain_and_sizes(g, draft):
 
 @pytest.mark.parametrize("draft", [False, True], ids=["guess", "draft"])
 @pytest.mark.parametrize("setting", [(0.0, 0, 1.0), (1.0, 0, 1.0), (1.0, 0, 0.5), (1.0, 700, 1.0),
-                                     (0.7, 901, 0.33)])
+                                     (0.7, 901, 0.33), (1.0, 1, 1.0), (1.0, 40, 1.0),
+                                     (0.7, 256, 0.33)])
 def test_verify_special_rows(g, draft, setting):
     """Equal logits in mass, NaN and infinities, the same token proposed twice,
     tokens out of range, numbers at the ends of [0, 1) and outside, a node that
@@ -412,6 +413,37 @@ def test_verify_top_k(g, draft, V, k, p):
     y[6] = z[6]
     par[:, 1:4] = 0
     check_verify(g, z, tok, par, u, 0.9, k, p, draft=y if draft else None, pad=3)
+    assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("k,p", [(0, 1.0), (0, 0.9), (20, 0.9), (300, 1.0)])
+def test_verify_calls_at_once_and_recorded(g, k, p):
+    """Calls on two streams at the same time, and one recorded and replayed on
+    other inputs, agree with calls alone."""
+    import torch
+    runs = []
+    for seed in (21, 22):
+        t = [cuda(x) for x in make_verify(seed, 40, 12, 2000, True)]
+        runs.append((t, torch.cuda.Stream()))
+    call = lambda t, **kw: g.tree_verify(t[0], 2000, t[2], t[4], 0.8, k, p, parent=t[3],
+                                         draft_logits=t[1], **kw)
+    want = [[x.clone() for x in call(t)] for t, _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [call(t, stream=s) for t, s in runs]
+        torch.cuda.synchronize()
+        for w, r in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(w, r))
+    own = [x.clone() for x in runs[0][0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(own)
+    for (t, _), w in zip(reversed(runs), reversed(want)):
+        for x, y in zip(own, t):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(w, out))
     assert g.device_error() == 0
 
 

@@ -257,6 +257,38 @@ def test_attention_stream_and_graph(g, dtype, N):
     assert g.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,H,Hkv,D", [(1, 4, 4, 64), (12, 4, 2, 64), (60, 4, 2, 128), (20, 2, 2, 16)])
+def test_attention_calls_at_once(g, dtype, N, H, Hkv, D):
+    """Calls on two streams at the same time, each with its own inputs."""
+    import torch
+    cases = [Case(dtype, 6, N, H, Hkv, D, 2000, [2000, 3, 900, 0, 64, 1500], seed=s) for s in (1, 2)]
+    args = [dict(c.args()) for c in cases]
+    lens = [cuda(c.lens) for c in cases]
+    call = lambda i, **kw: g.tree_attention(cases[i].qkv, cases[i].k, cases[i].v, lens[i], H,
+                                            **args[i], **kw)
+    want = [call(i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [call(i, stream=streams[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("N,G", [(1, 1), (3, 2), (40, 1)])
+def test_attention_tiny_caches(g, dtype, D, N, G):
+    """Caches of fewer rows than a tile, empty and full ones."""
+    for Tc, lens in ((1, [1]), (3, [0]), (5, [5, 2])):
+        c = Case(dtype, len(lens), N, G, 1, D, Tc, lens, seed=Tc + N)
+        c.check(*c.call(g))
+    assert g.device_error() == 0
+
+
 def test_attention_matches_the_causal_forward(g):
     """A chain behind an empty cache is the causal attention of training."""
     import torch

@@ -611,7 +611,7 @@ def sample(logits, vocab, temperature=0.8, top_k=0, top_p=0.9, uniform=None, out
 def _elsewhere(t, stream):
     """Whether a call on t's device needs another current device or stream."""
     import torch
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != torch._C._cuda_getDevice()
 
 
 def _on_device_of(t, stream):
@@ -727,7 +727,7 @@ def tree_attention(qkv, k_cache, v_cache, lens, n_head, parent=None, counts=None
     nbytes = _tree_attention_bytes(B, N, n_head, Hkv, D, dt)
     if out is None:
         new = qkv.new_empty if counts is None else qkv.new_zeros
-        out = new((B, N, n_head * D))
+        out = new(B, N, n_head * D)
         po = out.data_ptr()
     else:
         po = _arg("out", out, dtype, (B, N, n_head * D), dev)
@@ -786,7 +786,7 @@ def tree_verify(logits, vocab, tokens, uniform, temperature=0.8, top_k=0, top_p=
     pu = _arg("uniform", _required("uniform", uniform), torch.float32, (B, N), dev)
     pp = _arg("parent", parent, i32, (B, N), dev)
     pc = _arg("counts", counts, i32, (B,), dev)
-    path = tokens.new_empty((B, N))
+    path = tokens.new_empty(B, N)
     n_path = tokens.new_empty(B)
     nxt = tokens.new_empty(B)
     rc = lib.gpt2_tree_verify(logits.data_ptr(), ld, pd, ldd, pt, pp, pc, pu, B, N, vocab,

@@ -288,8 +288,8 @@ int simt_grid() { return Cfg<D, MR>::kCtas * gpt2_internal::sm_count(); }
 template <int D, int MR>
 int launch_simt(const TreeAttnArgs& a, cudaStream_t st) {
   const int smem = int(sizeof(typename Cfg<D, MR>::Smem));
-  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_simt_kernel<D, MR>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static std::atomic<uint64_t> allowed{0};
+  GPT2_CUDA_TRY(allow_smem(allowed, tree_attn_simt_kernel<D, MR>, smem));
   const int grid = simt_grid<D, MR>();
   const TreeAttnArgs w = with_workspace<MR>(a, grid);
   tree_attn_simt_kernel<D, MR><<<grid, kThreads, smem, st>>>(w);

@@ -479,8 +479,8 @@ struct Variant {
       gpt2_internal::set_error("tree_attention: tensor map encoding failed");
       return GPT2_ERR_CUDA;
     }
-    GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_mma_kernel<D, WM, WK>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem));
+    static std::atomic<uint64_t> allowed{0};
+  GPT2_CUDA_TRY(allow_smem(allowed, tree_attn_mma_kernel<D, WM, WK>, F::kSmem));
     const TreeAttnArgs w = with_workspace<F::MR>(a, grid());
     tree_attn_mma_kernel<D, WM, WK><<<grid(), F::kThreads, F::kSmem, st>>>(mk, mv, mx, w);
     COUNT_LAUNCH(1);

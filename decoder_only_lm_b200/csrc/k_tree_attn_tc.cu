@@ -658,8 +658,8 @@ int launch_tc(const TreeAttnArgs& a, cudaStream_t st) {
     gpt2_internal::set_error("tree_attention: tensor map encoding failed");
     return GPT2_ERR_CUDA;
   }
-  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_attn_tc_kernel<D, P>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem));
+  static std::atomic<uint64_t> allowed{0};
+  GPT2_CUDA_TRY(allow_smem(allowed, tree_attn_tc_kernel<D, P>, F::kSmem));
   const TreeAttnArgs w = with_workspace<F::MR>(a, grid_size());
   tree_attn_tc_kernel<D, P><<<grid_size(), kThreads, F::kSmem, st>>>(mk, mv, mx, w);
   COUNT_LAUNCH(1);

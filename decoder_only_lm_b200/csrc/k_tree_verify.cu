@@ -734,8 +734,10 @@ template <bool kDraft, bool kCuts>
 int launch(const TreeVerifyArgs& a, cudaStream_t st) {
   const int slice = cdiv(a.V, kCluster);
   const size_t smem = (size_t(slice) * sizeof(uint64_t) + (kCuts ? sizeof(Cut) : 0)) * (kDraft ? 2 : 1);
-  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_verify_kernel<kDraft, kCuts>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  constexpr size_t kMost =
+      (kTreeMaxVocab / kCluster * sizeof(uint64_t) + (kCuts ? sizeof(Cut) : 0)) * (kDraft ? 2 : 1);
+  static std::atomic<uint64_t> allowed{0};
+  GPT2_CUDA_TRY(allow_smem(allowed, tree_verify_kernel<kDraft, kCuts>, kMost));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

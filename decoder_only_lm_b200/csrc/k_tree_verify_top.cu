@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(kTopThreads, 2)
 template <bool kDraft>
 int launch(const TreeVerifyArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(List) * (kDraft ? 2 : 1);
-  GPT2_CUDA_TRY(cudaFuncSetAttribute(tree_verify_top_kernel<kDraft>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  static std::atomic<uint64_t> allowed{0};
+  GPT2_CUDA_TRY(allow_smem(allowed, tree_verify_top_kernel<kDraft>, smem));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

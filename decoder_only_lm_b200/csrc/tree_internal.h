@@ -6,9 +6,25 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 // error-word value of a length, count, parent or path that is out of range
 // (read back as GPT2_ERR_ARG; other values are bounded-wait timeouts)
 constexpr int kTreeBadInput = 0x7A00;
+
+// Allows a kernel its dynamic shared memory, once per device (`done`: the devices
+// that have it; more than 64 are asked every time).
+template <typename Kernel>
+cudaError_t allow_smem(std::atomic<uint64_t>& done, Kernel kernel, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 struct TreeAttnArgs {
   const void* qkv;

@@ -53,7 +53,7 @@ def test_tree_attention_workspace(g):
 @pytest.mark.parametrize("bad", [
     dict(logits=None), dict(tokens=None), dict(uniform=None), dict(path=None), dict(n=None),
     dict(next=None), dict(B=0), dict(N=0), dict(N=257), dict(V=0), dict(V=65537, ld=1 << 20),
-    dict(ld=99), dict(draft=P, ldd=99), dict(T=-0.5), dict(T=float("inf")), dict(T=float("nan")),
+    dict(ld=99), dict(draft=P, ldd=99), dict(T=-0.5), dict(T=float("inf")), dict(T=float("nan")), dict(T=2e20),
     dict(k=-1), dict(p=0.0), dict(p=1.5), dict(p=float("nan"))])
 def test_tree_verify_refuses(g, bad):
     a = dict(logits=P, ld=100, draft=None, ldd=0, tokens=P, uniform=P, B=1, N=4, V=100, T=1.0, k=0,

@@ -22,7 +22,8 @@
 // row + 64 i, and copy i takes its half of each tile's keys, with zeros for the
 // other among its probabilities, so the products stay the same instructions
 // (long trees of 48: 57.3 -> 53.9 us).  The copies' maxima, sums and outputs
-// merge at a piece's end.
+// merge at a piece's end, where sum_nonfinite looks after cached values that 0
+// times is not 0.
 // What a tile holds behind the last key (or the last node) is not the
 // sequence's: its scores are masked, and the row threads clear its value rows
 // before the product.  They also bring the query rows, the next piece's before
@@ -114,6 +115,51 @@ __device__ __forceinline__ bool elect_one() {
 template <typename T>
 __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
+}
+// Where a row's copies multiply each other's keys by 0, a cached value that is not
+// finite (0 times it is not 0) makes the row's sum NaN whatever its share is.  A
+// stored column that came out so becomes the sum of such values' shares, beside
+// which the finite ones do not count; without any it stays (an overflow).  By a
+// whole warp over the cached keys [k0, k1) of the piece, 32 at a time; `mine`: the
+// lane stored columns that are not finite, of those from 16 copy on, in every Pth
+// group of 16.  m: base of the row's result (log2 domain), times inv_l.
+template <int D, int P, typename Out>
+__device__ __noinline__ void sum_nonfinite(const TreeAttnArgs& a, int b, int hk, int hq, int node,
+                                           bool mine, int k0, int k1, float m, float inv_l, Out* dst,
+                                           int copy) {
+  constexpr int kCols = D / P;  // columns of a copy
+  auto column = [&](int i) { return 16 * (copy + P * (i / 16)) + i % 16; };
+  auto finite = [](float x) { return fabsf(x) <= 3.4028234e38f; };
+  const bf16* q = static_cast<const bf16*>(a.qkv) + (int64_t(b) * a.N + node) * a.ld_qkv + int64_t(hq) * D;
+  const int64_t row0 = (int64_t(b) * a.Hkv + hk) * a.Tc;
+  const bf16* kc = static_cast<const bf16*>(a.k) + row0 * D;
+  const bf16* vc = static_cast<const bf16*>(a.v) + row0 * D;
+  const float scale = rsqrtf(float(D)) * kLog2e;
+  uint64_t odd = 0, found = 0;
+  static_assert(kCols <= 64, "a bit for each column");
+  if (mine)
+    for (int i = 0; i < kCols; ++i)
+      if (!finite(to_f32<Out>(dst[column(i)]))) odd |= uint64_t(1) << i;
+  for (int j0 = k0; j0 < k1; j0 += 32) {
+    bool bad = false;
+    if (const int j = j0 + int(threadIdx.x) % 32; j < k1)
+      for (int i = 0; i < kCols; ++i) bad |= !finite(to_f32<bf16>(vc[int64_t(j) * D + column(i)]));
+    for (unsigned which = __ballot_sync(0xffffffffu, bad); which; which &= which - 1) {
+      const int64_t at = (j0 + int64_t(__ffs(int(which)) - 1)) * D;
+      if (!odd) continue;
+      float s = 0.f;
+      for (int d = 0; d < D; ++d) s = fmaf(to_f32<bf16>(q[d]), to_f32<bf16>(kc[at + d]), s);
+      const float p = ex2(fmaf(s, scale, -m)) * inv_l;
+      for (int i = 0; i < kCols; ++i) {
+        const float v = to_f32<bf16>(vc[at + column(i)]);
+        const uint64_t bit = uint64_t(1) << i;
+        if (!(odd & bit) || finite(v)) continue;
+        Out& x = dst[column(i)];
+        x = from_f32<Out>(found & bit ? fmaf(p, v, to_f32<Out>(x)) : p * v);
+        found |= bit;
+      }
+    }
+  }
 }
 template <int D, int P>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -569,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         f = m == -INFINITY ? 0.f : ex2(m - M);
       }
       if (whole) f /= L;
+      float odd = 0.f;  // NaN: the thread stored columns that are not finite (P > 1)
 #pragma unroll
       for (int c = 0; c < D; c += 16) {
         float x[16];
@@ -605,6 +652,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (F::kXch == 1) rows_sync();
         }
         if (!real || copy != (c / 16) % P) continue;
+        if constexpr (P > 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) odd = fmaf(x[i], 0.f, odd);
+        }
         if (whole) {
 #pragma unroll
           for (int i = 0; i < 16; i += 8)
@@ -620,6 +671,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (!ok) break;
       tc_fence_before();
+      if constexpr (P > 1) {
+        if (__any_sync(0xffffffffu, odd != 0.f)) {
+          const int k0 = p.t0 * KT, k1 = t1 <= ct ? min(len, t1 * KT) : len;
+          if (whole)
+            sum_nonfinite<D, P>(a, p.b, p.hk, hq, node, odd != 0.f, k0, k1, M, 1.f / L, out, copy);
+          else
+            sum_nonfinite<D, P>(a, p.b, p.hk, hq, node, odd != 0.f, k0, k1, M, 1.f,
+                                w + int64_t(row) * D, copy);
+        }
+      }
       if (real) {
         if (copy == 0) {
           if (whole) {

@@ -665,3 +665,39 @@ def test_decoding_with_drafts_matches_greedy_generation(g):
     assert steps < n_new  # several tokens a step
     assert g.device_error() == 0
     gm.close()
+
+
+# ---------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("N", [1, 20, 48, 80])
+@pytest.mark.parametrize("lens", [[700, 64, 1], [9000, 33, 95]])
+def test_attention_infinite_cached_values(g, dtype, D, N, lens):
+    """Infinite and NaN values in cache rows that every node sees: the same sums
+    whatever the number of rows, an infinity of its sign, NaN for two signs or
+    a NaN, and the other channels as without them."""
+    c = Case(dtype, len(lens), N, 4, 4, D, max(lens), lens, seed=D + N)
+    inf, nan = float("inf"), float("nan")
+    clean = [t.clone() for t in c.call(g)]
+    want = {}
+    for b, L in enumerate(lens):
+        # keys in either half of a tile, and the last one
+        first, second, last = 5 % L, 40 % L, L - 1
+        c.v[b, :, first, 2] = inf
+        c.v[b, :, second, 3] = -inf
+        c.v[b, :, first, 6] = c.v[b, :, last, 6] = inf
+        c.v[b, :, last, 7] = nan
+        want[b] = {2: inf, 3: -inf, 6: inf, 7: nan}
+        if last != first:
+            c.v[b, :, first, 9], c.v[b, :, last, 9] = inf, -inf
+            want[b][9] = nan
+    out, lse = c.call(g)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    for b in range(len(lens)):
+        x = out[b].reshape(N, 4, D)
+        y = clean[0][b].float().cpu().numpy().reshape(N, 4, D)
+        for d, value in want[b].items():
+            y[..., d] = value
+        np.testing.assert_array_equal(x, y, err_msg=f"sequence {b}")
+    np.testing.assert_array_equal(lse, clean[1].cpu().numpy())
+    assert g.device_error() == 0

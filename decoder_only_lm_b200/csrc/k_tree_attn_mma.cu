@@ -238,42 +238,35 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
       const uint32_t sk = sring + s * 2 * F::kTile, sv = sk + F::kTile;
       if (!plain(p, t)) {
         // Value rows behind the last key are foreign, and a node that a row may not
-        // see can hold anything: what is not this sequence's, and node values that
-        // are not finite (see add_nonfinite), become 0 for the product.
+        // see can hold anything: the rows that are not this sequence's, and node
+        // values that are not finite (see add_nonfinite), become 0 for the product.
         uint8_t* vt = ring + (sv - sring);
-        uint64_t drop = nk >= KT ? 0 : ~uint64_t(0) << nk;
-        if (fresh) {
-          uint64_t* word = bad + (k0 >> 6);
-          if (t == max(p.t0, p.ct)) {  // the piece's first: no other tile's words count
-            sync();                    // (the last piece's words and masks have been read)
-            if (tid < kMaxNodes / 64) bad[tid] = 0;
-            if (new_masks) {
-              build_masks(parents, p.n, mask, up, flag, a.err, tid, 32 * NW, sync);
-              mask_of = p.b;
+        uint64_t* word = bad + (k0 >> 6);
+        if (fresh && t == max(p.t0, p.ct)) {  // the piece's first: no other tile's words count
+          sync();                             // (the last piece's words and masks have been read)
+          if (tid < kMaxNodes / 64) bad[tid] = 0;
+          if (new_masks) {
+            build_masks(parents, p.n, mask, up, flag, a.err, tid, 32 * NW, sync);
+            mask_of = p.b;
+          }
+          sync();
+        }
+        for (int e = tid; e < KT * C; e += 32 * NW) {
+          const int r = e / C;
+          uint4* at_e = reinterpret_cast<uint4*>(vt + at<D>(r, e % C));
+          if (r >= nk) {
+            *at_e = make_uint4(0, 0, 0, 0);
+          } else if (fresh) {
+            uint4 u = *at_e;
+            if (drop_nonfinite(u)) {
+              *at_e = u;
+              atomicOr(reinterpret_cast<unsigned long long*>(word), 1ull << r);
             }
-            sync();
-          }
-          for (int e = tid; e < KT * C; e += 32 * NW) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vt + at<D>(e / C, e % C));
-            auto inf = [](uint32_t w) {
-              return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-            };
-            if (e / C < nk && (inf(u.x) || inf(u.y) || inf(u.z) || inf(u.w)))
-              atomicOr(reinterpret_cast<unsigned long long*>(word), 1ull << (e / C));
-          }
-          sync();
-          if (*word) {
-            any_bad = true;
-            drop |= *word;
           }
         }
-        if (drop) {
-          for (int e = tid; e < KT * C; e += 32 * NW)
-            if ((drop >> (e / C)) & 1)
-              *reinterpret_cast<uint4*>(vt + at<D>(e / C, e % C)) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async();  // before the stage is handed back
-          sync();
-        }
+        fence_proxy_async();  // before the stage is handed back
+        sync();
+        if (fresh && *word) any_bad = true;
         if (!ok) break;
       }
       if (busy && nw > 0) {

@@ -22,7 +22,7 @@
 // row + 64 i, and copy i takes its half of each tile's keys, with zeros for the
 // other among its probabilities, so the products stay the same instructions
 // (long trees of 48: 57.3 -> 53.9 us).  The copies' maxima, sums and outputs
-// merge at a piece's end, where sum_nonfinite looks after cached values that 0
+// merge at a piece's end, where share_nonfinite looks after cached values that 0
 // times is not 0.
 // What a tile holds behind the last key (or the last node) is not the
 // sequence's: its scores are masked, and the row threads clear its value rows
@@ -116,50 +116,73 @@ template <typename T>
 __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
+// Values that are not finite, behind the stores of a piece's results (of row
+// `node`, base m in the log2 domain, times inv_l; `mine`: this lane stored some, the
+// columns from 16 copy on in every Pth group of 16).  By a whole warp.
+//
 // Where a row's copies multiply each other's keys by 0, a cached value that is not
 // finite (0 times it is not 0) makes the row's sum NaN whatever its share is.  A
-// stored column that came out so becomes the sum of such values' shares, beside
-// which the finite ones do not count; without any it stays (an overflow).  By a
-// whole warp over the cached keys [k0, k1) of the piece, 32 at a time; `mine`: the
-// lane stored columns that are not finite, of those from 16 copy on, in every Pth
-// group of 16.  m: base of the row's result (log2 domain), times inv_l.
+// column that came out not finite becomes the sum of such values' shares, beside
+// which the finite ones do not count; without any it stays (an overflow).  Then the
+// shares of the nodes in `bad`, if any_bad (see add_nonfinite).
 template <int D, int P, typename Out>
-__device__ __noinline__ void sum_nonfinite(const TreeAttnArgs& a, int b, int hk, int hq, int node,
-                                           bool mine, int k0, int k1, float m, float inv_l, Out* dst,
-                                           int copy) {
-  constexpr int kCols = D / P;  // columns of a copy
-  auto column = [&](int i) { return 16 * (copy + P * (i / 16)) + i % 16; };
-  auto finite = [](float x) { return fabsf(x) <= 3.4028234e38f; };
-  const bf16* q = static_cast<const bf16*>(a.qkv) + (int64_t(b) * a.N + node) * a.ld_qkv + int64_t(hq) * D;
-  const int64_t row0 = (int64_t(b) * a.Hkv + hk) * a.Tc;
-  const bf16* kc = static_cast<const bf16*>(a.k) + row0 * D;
-  const bf16* vc = static_cast<const bf16*>(a.v) + row0 * D;
-  const float scale = rsqrtf(float(D)) * kLog2e;
-  uint64_t odd = 0, found = 0;
-  static_assert(kCols <= 64, "a bit for each column");
-  if (mine)
-    for (int i = 0; i < kCols; ++i)
-      if (!finite(to_f32<Out>(dst[column(i)]))) odd |= uint64_t(1) << i;
-  for (int j0 = k0; j0 < k1; j0 += 32) {
-    bool bad = false;
-    if (const int j = j0 + int(threadIdx.x) % 32; j < k1)
-      for (int i = 0; i < kCols; ++i) bad |= !finite(to_f32<bf16>(vc[int64_t(j) * D + column(i)]));
-    for (unsigned which = __ballot_sync(0xffffffffu, bad); which; which &= which - 1) {
-      const int64_t at = (j0 + int64_t(__ffs(int(which)) - 1)) * D;
-      if (!odd) continue;
-      float s = 0.f;
-      for (int d = 0; d < D; ++d) s = fmaf(to_f32<bf16>(q[d]), to_f32<bf16>(kc[at + d]), s);
-      const float p = ex2(fmaf(s, scale, -m)) * inv_l;
-      for (int i = 0; i < kCols; ++i) {
-        const float v = to_f32<bf16>(vc[at + column(i)]);
-        const uint64_t bit = uint64_t(1) << i;
-        if (!(odd & bit) || finite(v)) continue;
-        Out& x = dst[column(i)];
-        x = from_f32<Out>(found & bit ? fmaf(p, v, to_f32<Out>(x)) : p * v);
-        found |= bit;
+__device__ void share_nonfinite(const TreeAttnArgs& a, const Piece& p, int hq, int node, bool mine,
+                                bool any_bad, const uint64_t* bad, const uint32_t* mask, float m,
+                                float inv_l, Out* dst, int copy) {
+  if constexpr (P > 1) {
+    constexpr int kCols = D / P;  // columns of a copy
+    static_assert(kCols <= 64, "a bit for each column");
+    auto column = [&](int i) { return 16 * (copy + P * (i / 16)) + i % 16; };
+    const bf16* q = static_cast<const bf16*>(a.qkv) + (int64_t(p.b) * a.N + node) * a.ld_qkv + int64_t(hq) * D;
+    const int64_t row0 = (int64_t(p.b) * a.Hkv + p.hk) * a.Tc;
+    const bf16* kc = static_cast<const bf16*>(a.k) + row0 * D;
+    const bf16* vc = static_cast<const bf16*>(a.v) + row0 * D;
+    const float scale = rsqrtf(float(D)) * kLog2e;
+    uint64_t odd = 0, found = 0;
+    if (mine)
+      for (int i = 0; i < kCols; ++i)
+        if (!finite(dst[column(i)])) odd |= uint64_t(1) << i;
+    // the piece's cached keys, 32 at a time
+    const int k1 = p.t1 <= p.ct ? min(p.len, p.t1 * KT) : p.len;
+    for (int j0 = __any_sync(0xffffffffu, odd != 0) ? p.t0 * KT : k1; j0 < k1; j0 += 32) {
+      bool hit = false;
+      if (const int j = j0 + int(threadIdx.x) % 32; j < k1)
+        for (int i = 0; i < kCols; ++i) hit |= !finite(vc[int64_t(j) * D + column(i)]);
+      for (unsigned which = __ballot_sync(0xffffffffu, hit); which; which &= which - 1) {
+        const int64_t at = (j0 + int64_t(__ffs(int(which)) - 1)) * D;
+        if (!odd) continue;
+        float s = 0.f;
+        for (int d = 0; d < D; ++d) s = fmaf(to_f32<bf16>(q[d]), to_f32<bf16>(kc[at + d]), s);
+        const float pj = ex2(fmaf(s, scale, -m)) * inv_l;
+        for (int i = 0; i < kCols; ++i) {
+          const bf16 v = vc[at + column(i)];
+          const uint64_t bit = uint64_t(1) << i;
+          if (!(odd & bit) || finite(v)) continue;
+          Out& x = dst[column(i)];
+          x = from_f32<Out>(found & bit ? fmaf(pj, to_f32<bf16>(v), to_f32<Out>(x)) : pj * to_f32<bf16>(v));
+          found |= bit;
+        }
       }
     }
   }
+  if (any_bad && mine)
+    for (int c = 16 * copy; c < D; c += 16 * P)
+      add_nonfinite<bf16, Out>(a, p.b, p.hk, hq, node, p.n, bad, mask, m, inv_l, dst, c, c + 16);
+}
+template <int D, int P>
+__device__ __noinline__ void share_nonfinite(const TreeAttnArgs& a, const Listed& p, int row, int copy,
+                                             bool any_bad, const uint64_t* bad, const uint32_t* mask,
+                                             float m, float l) {
+  constexpr int MR = Cfg<D, P>::MR;
+  const bool mine = row < p.rows;
+  const int gr = p.rt * MR + (mine ? row : 0), node = gr / a.G, hq = p.hk * a.G + gr % a.G;
+  if (p.whole())
+    share_nonfinite<D, P>(a, p, hq, node, mine, any_bad, bad, mask, m, 1.f / l,
+                          static_cast<bf16*>(a.out) + (int64_t(p.b) * a.N + node) * a.ld_out + int64_t(hq) * D,
+                          copy);
+  else
+    share_nonfinite<D, P>(a, p, hq, node, mine, any_bad, bad, mask, m, 1.f,
+                          a.ws + p.slot * slot_floats<MR>(D) + int64_t(row) * D, copy);
 }
 template <int D, int P>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -416,37 +439,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (e == 0) mbar_arrive(b_q);
     };
     // A tile with foreign rows, or with nodes that a row may not see: value rows
-    // behind the last key become 0, and so do node rows with non-finite values,
-    // which are noted in `bad` (see add_nonfinite).
+    // behind the last key become 0, and so do node values that are not finite, whose
+    // nodes are noted in `bad` (see add_nonfinite).
     auto clear = [&](const Piece& q, int t, int gt) -> bool {
       const int s = gt % NS;
       const bool fresh = t >= q.ct;
       const int nk = fresh ? q.n - (t - q.ct) * KT : q.len - t * KT;
       wait(b_vf(s), (gt / NS) & 1, 21);
       uint8_t* v = ring + s * 2 * F::kTile + F::kTile;
-      uint64_t drop = nk >= KT ? 0 : ~uint64_t(0) << nk;
-      bool found = false;
-      if (fresh) {
-        uint64_t* word = bad + (t - q.ct);
-        for (int x = e; x < KT * D / 8; x += kLanes) {  // 16-byte units, the swizzle left alone
-          const int r = x / 8 % KT;
-          const uint4 u = *reinterpret_cast<const uint4*>(v + x * 16);
-          auto inf = [](uint32_t w2) {
-            return (w2 & 0x7F80u) == 0x7F80u || (w2 & 0x7F800000u) == 0x7F800000u;
-          };
-          if (r < nk && (inf(u.x) || inf(u.y) || inf(u.z) || inf(u.w)))
+      uint64_t* word = bad + (fresh ? t - q.ct : 0);
+      for (int x = e; x < KT * D / 8; x += kLanes) {  // 16-byte units, the swizzle left alone
+        const int r = x / 8 % KT;
+        uint4* at = reinterpret_cast<uint4*>(v + x * 16);
+        if (r >= nk) {
+          *at = make_uint4(0, 0, 0, 0);
+        } else if (fresh) {
+          uint4 u = *at;
+          if (drop_nonfinite(u)) {
+            *at = u;
             atomicOr(reinterpret_cast<unsigned long long*>(word), 1ull << r);
+          }
         }
-        rows_sync();
-        found = *word != 0;
-        drop |= *word;
       }
-      if (drop) {
-        for (int x = e; x < KT * D / 8; x += kLanes)
-          if ((drop >> (x / 8 % KT)) & 1) *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async();  // before this thread's arrival that the product waits for
-      }
-      return found;
+      fence_proxy_async();  // before this thread's arrival that the product waits for
+      if (!fresh) return false;
+      rows_sync();
+      return *word != 0;
     };
     wait(b_listed(0), 0, 26);
     if (ok && list[0].kt > 0) {
@@ -653,8 +671,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!real || copy != (c / 16) % P) continue;
         if constexpr (P > 1) {
+          float y[4];  // (a sum with infinities or NaN is one)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) odd = fmaf(x[i], 0.f, odd);
+          for (int i = 0; i < 4; ++i) y[i] = (x[i] + x[i + 4]) + (x[i + 8] + x[i + 12]);
+          odd = fmaf((y[0] + y[1]) + (y[2] + y[3]), 0.f, odd);
         }
         if (whole) {
 #pragma unroll
@@ -671,16 +691,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (!ok) break;
       tc_fence_before();
-      if constexpr (P > 1) {
-        if (__any_sync(0xffffffffu, odd != 0.f)) {
-          const int k0 = p.t0 * KT, k1 = t1 <= ct ? min(len, t1 * KT) : len;
-          if (whole)
-            sum_nonfinite<D, P>(a, p.b, p.hk, hq, node, odd != 0.f, k0, k1, M, 1.f / L, out, copy);
-          else
-            sum_nonfinite<D, P>(a, p.b, p.hk, hq, node, odd != 0.f, k0, k1, M, 1.f,
-                                w + int64_t(row) * D, copy);
-        }
-      }
       if (real) {
         if (copy == 0) {
           if (whole) {
@@ -690,15 +700,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             w[MR * D + MR + row] = L;
           }
         }
-        if (any_bad)
-          for (int c = 16 * copy; c < D; c += 16 * P) {  // the columns that this thread stored
-            if (whole)
-              add_nonfinite<bf16, bf16>(a, p.b, p.hk, hq, node, pn, bad, mask, M, 1.f / L, out, c, c + 16);
-            else
-              add_nonfinite<bf16, float>(a, p.b, p.hk, hq, node, pn, bad, mask, M, 1.f,
-                                         w + int64_t(row) * D, c, c + 16);
-          }
       }
+      if (__any_sync(0xffffffffu, any_bad || odd != 0.f))
+        share_nonfinite<D, P>(a, p, row, copy, any_bad, bad, mask, M, L);
     }
   }
   tc_fence_before();

@@ -306,8 +306,12 @@ __device__ __forceinline__ uint64_t sees(bool chain, const uint32_t* mask, int i
 // times such a value is not 0, and most rows may not see the node); the rows that
 // see one get its share here, after their results were stored by this thread:
 // channels [c0, c1) of a row whose result has base m (log2 domain), times inv_l,
-// the probability once more from the query and the key.  bad: 64 bits per 64
-// nodes.
+// the probability once more from the query and the key.  bad: the nodes that hold
+// such values, 64 bits per 64 nodes.
+template <typename T>
+__device__ __forceinline__ bool finite(T x) {
+  return fabsf(to_f32<T>(x)) <= 3.4028234e38f;
+}
 template <typename T, typename Out>
 __device__ __noinline__ void add_nonfinite(const TreeAttnArgs& a, int b, int hk, int hq, int node,
                                            int n, const uint64_t* bad, const uint32_t* mask, float m,
@@ -325,9 +329,19 @@ __device__ __noinline__ void add_nonfinite(const TreeAttnArgs& a, int b, int hk,
       for (int d = 0; d < a.D; ++d) s = fmaf(to_f32<T>(q[d]), to_f32<T>(k[d]), s);
       const float p = exp2f(fmaf(s, scale, -m)) * inv_l;
       if (p != 0.f)
-        for (int c = c0; c < c1; ++c) dst[c] = from_f32<Out>(fmaf(p, to_f32<T>(v[c]), to_f32<Out>(dst[c])));
+        for (int c = c0; c < c1; ++c)
+          if (!finite(v[c])) dst[c] = from_f32<Out>(fmaf(p, to_f32<T>(v[c]), to_f32<Out>(dst[c])));
     }
   }
+}
+// 8 bf16 values with those that are not finite (exponent bits all ones: one more
+// carries into the sign's place) replaced by 0; whether there are any.
+__device__ __forceinline__ bool drop_nonfinite(uint4& u) {
+  auto carry = [](uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; };
+  if (((carry(u.x) | carry(u.y) | carry(u.z) | carry(u.w)) & 0x80008000u) == 0) return false;
+  auto clean = [&](uint32_t& w) { w &= ~(((carry(w) >> 15) & 0x00010001u) * 0xFFFFu); };
+  clean(u.x), clean(u.y), clean(u.z), clean(u.w);
+  return true;
 }
 
 // Workspace: 2 slots per CTA, each MR x D fp32 outputs, then the rows' running

@@ -701,3 +701,24 @@ def test_attention_infinite_cached_values(g, dtype, D, N, lens):
         np.testing.assert_array_equal(x, y, err_msg=f"sequence {b}")
     np.testing.assert_array_equal(lse, clean[1].cpu().numpy())
     assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("N", [4, 9, 20, 40, 70])
+def test_attention_node_with_infinite_values(g, dtype, D, N):
+    """One infinite or NaN value of a node: rows that see it have it in that
+    channel, and everything else is what it is with a finite value there."""
+    c = Case(dtype, 3, N, 4, 2, D, 400, [300, 0, 77], seed=D + N, tree="random")
+    out, lse = [t.clone() for t in c.call(g)]
+    v = c.qkv[..., (c.H + c.Hkv) * D:].view(3, N, c.Hkv, D)
+    want = out.float().view(3, N, c.H, D).cpu().numpy()
+    see = np.stack([tree_ref.ancestors(par) for par in c.par])
+    for node, channel, value in ((1, 5, float("inf")), (2, 6, -float("inf")), (N - 1, 0, float("nan"))):
+        v[:, node, :, channel] = value
+        for b in range(3):
+            want[b, see[b, :, node], :, channel] = value
+    got, got_lse = c.call(g)
+    np.testing.assert_array_equal(got.float().view(3, N, c.H, D).cpu().numpy(), want)
+    np.testing.assert_array_equal(got_lse.cpu().numpy(), lse.cpu().numpy())
+    assert g.device_error() == 0

@@ -554,8 +554,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float mn = __fmul_rn(fmaxf(c2[0], c2[1]), scale);
           const bool resc = mn > m + kRescale;
           if (__any_sync(0xffffffffu, resc)) {
-            const float corr = resc ? ex2(m - mn) : 1.f;
-            if (resc) m = mn;
+            // (between the halves by a whole number: the first half's probabilities are
+            // in bf16 already, and scaled by a power of two they are not rounded again)
+            const float by = h == 1 && m != -INFINITY ? ceilf(mn - m) : mn - m;
+            const float corr = resc ? ex2(-by) : 1.f;
+            if (resc) m = m != -INFINITY ? m + by : mn;
             l *= corr;
             if (h == 1) {  // the first half's probabilities had the old base
               uint32_t q[16];

@@ -722,3 +722,29 @@ def test_attention_node_with_infinite_values(g, dtype, D, N):
     np.testing.assert_array_equal(got.float().view(3, N, c.H, D).cpu().numpy(), want)
     np.testing.assert_array_equal(got_lse.cpu().numpy(), lse.cpu().numpy())
     assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,B", [(1, 64), (12, 8), (80, 16)])
+def test_attention_late_maximum(g, D, N, B):
+    """A maximum in a tile's second half far above the first half's, where the
+    values are: the probabilities of the first are rounded once (a second
+    rounding takes about one sum in 500 out of check()'s bound)."""
+    import torch
+    c = Case("bf16", B, N, 4, 1, D, 130, [64 if b % 2 else 130 for b in range(B)], seed=D)
+    q = c.qkv[..., :4 * D].view(B, N, 4, D)
+    e = torch.eye(D, device="cuda")[:3].bfloat16()
+    gen = torch.Generator("cuda").manual_seed(N)
+    u = torch.rand((2, B, N, 4), device="cuda", generator=gen)
+    q.zero_()
+    q[..., 0], q[..., 1], q[..., 2] = 4 * u[0] + 0.1, 2 * u[1] + 4, 1
+    # scores: key 0 of every sequence 0, key 1 a few bits below it, key 32 some 11
+    # to 18 bits above, all others (the nodes too) 12 to 18 bits below
+    c.k[:] = -100 * e[2]
+    c.qkv[..., 4 * D:5 * D] = -100 * e[2]
+    c.k[:, :, 0], c.k[:, :, 1], c.k[:, :, 32] = 0, -4 * e[0], (16 if D == 64 else 24) * e[1]
+    c.v.zero_()
+    c.qkv[..., 5 * D:] = 0
+    c.v[:, :, 1] = 1 + torch.arange(D, device="cuda") / D
+    c.check(*c.call(g))
+    assert g.device_error() == 0

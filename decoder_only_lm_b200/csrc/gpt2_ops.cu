@@ -14,13 +14,13 @@
 
 #include "attn_internal.h"
 #include "kernels.h"
-#include "tree_internal.h"
 
 using gpt2_internal::set_error;
 
 namespace {
 
-__device__ int g_op_error;  // bounded-wait timeouts of op-level launches
+// bounded-wait timeouts of op-level launches, and device-side contents out of range
+__device__ int g_op_error[2];
 
 }  // namespace
 
@@ -275,11 +275,11 @@ int gpt2_device_error(int* code) {
   if (!code) return GPT2_ERR_ARG;
   int* w = device_error_word();
   if (!w) return GPT2_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpy(&v, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GPT2_ERR_CUDA;
-  int z = 0;
-  cudaMemcpy(w, &z, sizeof(int), cudaMemcpyHostToDevice);
-  *code = v == kTreeBadInput ? GPT2_ERR_ARG : v ? GPT2_ERR_TIMEOUT : GPT2_OK;
+  int v[2] = {0, 0};
+  if (cudaMemcpy(v, w, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return GPT2_ERR_CUDA;
+  const int z = 0;
+  if (v[0] || v[1]) cudaMemcpy(v[0] ? w : w + 1, &z, sizeof(int), cudaMemcpyHostToDevice);
+  *code = v[0] ? GPT2_ERR_TIMEOUT : v[1] ? GPT2_ERR_ARG : GPT2_OK;
   return GPT2_OK;
 }
 

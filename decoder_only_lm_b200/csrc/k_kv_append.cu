@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(KvAppendArgs a, 
   const bool lead = blockIdx.x == 0 && l == 0 && threadIdx.x == 0;
   if (len < 0 || n < 0 || n > a.N || len + n > a.Tc) {
     if (lead) {
-      atomicExch(a.err, kTreeBadInput);
+      note_bad_input(a.err);
       if (a.new_lens) a.new_lens[b] = int32_t(len);
     }
     return;
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(KvAppendArgs a, 
   for (int r = blockIdx.x * kWarps + (threadIdx.x >> 5); r < n; r += gridDim.x * kWarps) {
     const int node = a.path ? a.path[int64_t(b) * a.N + r] : r;
     if (node < 0 || node >= a.N) {
-      if (lane == 0) atomicExch(a.err, kTreeBadInput);
+      if (lane == 0) note_bad_input(a.err);
       continue;
     }
     const uint4* src = reinterpret_cast<const uint4*>(x + int64_t(node) * a.ld_qkv * eb);

@@ -157,7 +157,7 @@ struct Split {
       in = scan(t);
       total += __shfl_sync(0xffffffffu, in, 31);
     }
-    if (bad && blockIdx.x == 0) atomicExch(a.err, kTreeBadInput);
+    if (bad && blockIdx.x == 0) note_bad_input(a.err);
     q.total = total;
     q.ctas = int(min64(total, gridDim.x));
     if (int(blockIdx.x) >= q.ctas) return q;  // an empty run
@@ -226,7 +226,7 @@ __device__ __forceinline__ void build_masks(const Parents& parents, int n, uint3
     int p = parents.p[k];
     if (i < n) {
       if (p < -1 || p >= i) {
-        atomicExch(err, kTreeBadInput);
+        note_bad_input(err);
         p = -1;
       }
       up[i] = p;

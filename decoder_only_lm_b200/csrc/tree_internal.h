@@ -8,9 +8,10 @@
 
 #include <atomic>
 
-// error-word value of a length, count, parent or path that is out of range
-// (read back as GPT2_ERR_ARG; other values are bounded-wait timeouts)
-constexpr int kTreeBadInput = 0x7A00;
+// A length, count, parent or path out of range, noted in its own word behind the
+// error word (err): a timeout recorded there stays, and calls that look for one
+// leave this alone.  Read back as GPT2_ERR_ARG.
+__device__ __forceinline__ void note_bad_input(int* err) { atomicExch(err + 1, 1); }
 
 // Allows a kernel its dynamic shared memory, once per device (`done`: the devices
 // that have it; more than 64 are asked every time).

@@ -130,7 +130,7 @@ __device__ __forceinline__ int load_tree(const TreeVerifyArgs& a, Tree& t, int b
     if (i < N && (p < -1 || p >= i)) bad = true;
     t.par[i] = p;
   }
-  if (bad && rank == 0) atomicExch(a.err, kTreeBadInput);
+  if (bad && rank == 0) note_bad_input(a.err);
   if (tid < 64) t.exp_table[tid] = Exp::entry(tid);
   if (N == 0 && rank == 0 && tid == 0) {
     a.n_path[b] = 0;

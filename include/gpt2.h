@@ -630,10 +630,12 @@ int gpt2_wait_selfcheck(int* expired);
  * them per handle). */
 int gpt2_launch_count(int64_t* n);
 
-/* Reads and clears the device error word shared by the op-level calls:
- * *code = GPT2_OK when nothing was recorded, GPT2_ERR_TIMEOUT for a bounded
- * wait that gave up, GPT2_ERR_ARG for device-side contents out of range (the
- * calls on drafted tokens); the last record wins.  Synchronises the device. */
+/* Reads and clears a record of the op-level calls: *code = GPT2_OK when there
+ * is none, GPT2_ERR_TIMEOUT for a bounded wait that gave up, GPT2_ERR_ARG for
+ * device-side contents out of range (the calls on drafted tokens).  With both
+ * recorded the timeout comes first and the other with the next call.  A call on
+ * a handle reports (and clears) a timeout too, never contents out of range.
+ * Synchronises the device. */
 int gpt2_device_error(int* code);
 
 #ifdef __cplusplus

@@ -748,3 +748,45 @@ def test_attention_late_maximum(g, D, N, B):
     c.v[:, :, 1] = 1 + torch.arange(D, device="cuda") / D
     c.check(*c.call(g))
     assert g.device_error() == 0
+
+
+# ---------------------------------------------------------------- records of bad input
+def test_bad_input_is_no_timeout(g):
+    """What a call on drafted tokens finds out of range stays on record until it
+    is asked for: calls on a handle neither fail for it nor clear it, and a wait
+    that gives up is told apart from it."""
+    import torch
+    gm = g.GPT2(2, 64, 4, 512, 512, 64, bf16=True, max_B=2, max_Tseq=32)
+    gm.set_params(synth.init_params(0, gm.shapes()))
+    x = cuda(np.random.default_rng(0).integers(0, 512, size=(2, 32)).astype(np.int32))
+    c = Case("bf16", 2, 6, 2, 2, 64, 100, [50, -1], seed=3)
+
+    def attention():
+        c.call(g)
+
+    def parents():
+        c.lens[1], c.par[1, 2] = 5, 4
+        c.call(g)
+
+    def verify():
+        z, _, tok, par, u = make_verify(2, 1, 6, 100, False)
+        g.tree_verify(cuda(z), 100, cuda(tok), cuda(u), parent=cuda(par), counts=cuda(np.array([9], np.int32)))
+
+    def append():
+        kv = torch.zeros((2, 1, 2, 2, 8, 64), device="cuda")
+        g.kv_append(torch.zeros((1, 2, 3, 384), device="cuda"), kv[0], kv[1],
+                    cuda(np.array([6, 0], np.int32)))
+
+    for call in (attention, parents, verify, append):
+        assert g.device_error() == 0
+        call()
+        assert np.isfinite(gm.forward_loss(x, x))
+        gm.generate(x[:, :8].contiguous(), 3, temperature=0.0, cached=True)
+        assert g.device_error() == g.ERR_ARG, call.__name__
+        assert g.device_error() == 0
+    c.lens[1] = -1
+    attention()
+    assert g.wait_selfcheck()
+    assert g.device_error() == g.ERR_ARG
+    assert g.device_error() == 0
+    gm.close()

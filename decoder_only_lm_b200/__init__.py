@@ -24,6 +24,7 @@ PROF_NAMES = ["gemm", "lmhead", "attn_fwd", "attn_bwd", "ln_fwd", "ln_bwd", "emb
 OK, ERR_ARG, ERR_TOKEN, ERR_NONFINITE, ERR_CUDA, ERR_OOM, ERR_TIMEOUT, ERR_STATE = range(8)
 PARAM, GRAD, ADAM_M, ADAM_V = range(4)
 F32, BF16 = 0, 1
+ZERO_ROWS = 256
 
 ALLOC_FN = C.CFUNCTYPE(C.c_void_p, C.c_size_t, C.c_void_p)
 FREE_FN = C.CFUNCTYPE(None, C.c_void_p, C.c_void_p)
@@ -702,8 +703,9 @@ def tree_attention(qkv, k_cache, v_cache, lens, n_head, parent=None, counts=None
     before each node, -1 for one that follows the cache (None: a chain, the
     causal chunk; N = 1: single-token decoding); counts: int32 [B] real nodes of
     each sequence (None: all).  Returns (out [B, N, n_head D], lse fp32
-    [B, n_head, N]); rows of nodes beyond counts are left as they were (0 in
-    buffers allocated here)."""
+    [B, n_head, N]); rows without a node (beyond counts, and all of a sequence
+    whose length or count is out of range) are left as they were in buffers that
+    are passed in, and 0 in buffers allocated here."""
     import torch
     if not qkv.is_cuda:
         raise ValueError(f"qkv: needs a cuda tensor, got one on {qkv.device}")
@@ -725,14 +727,16 @@ def tree_attention(qkv, k_cache, v_cache, lens, n_head, parent=None, counts=None
     pp = _arg("parent", parent, i32, (B, N), dev)
     pc = _arg("counts", counts, i32, (B,), dev)
     nbytes = _tree_attention_bytes(B, N, n_head, Hkv, D, dt)
+    if out is None and lse is None:  # the call fills every row
+        new, dt = qkv.new_empty, dt | ZERO_ROWS
+    else:  # ... or leaves the rows without a node of both buffers
+        new = qkv.new_zeros
     if out is None:
-        new = qkv.new_empty if counts is None else qkv.new_zeros
         out = new(B, N, n_head * D)
         po = out.data_ptr()
     else:
         po = _arg("out", out, dtype, (B, N, n_head * D), dev)
     if lse is None:
-        new = qkv.new_empty if counts is None else qkv.new_zeros
         lse = new((B, n_head, N), dtype=f32)
         pe = lse.data_ptr()
     else:

@@ -48,6 +48,8 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
                         void* stream) {
   if (!qkv || !k_cache || !v_cache || !lens || !out)
     return refuse("tree_attention: null pointer");
+  const bool zero = dtype & GPT2_ZERO_ROWS;
+  dtype &= ~GPT2_ZERO_ROWS;
   if (!type_ok(dtype)) return refuse("tree_attention: bad dtype");
   if (!heads_ok(B, N, H, Hkv, D) || Tc < 1 || int64_t(B) * Hkv * Tc > int64_t(0x7FFFFFFF))
     return refuse("tree_attention: B, N (1..256), H, Hkv, D (16, 32, 64, 128) or Tc out of range");
@@ -61,7 +63,8 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
     return refuse("tree_attention: workspace too small");
   try {
     TreeAttnArgs a{qkv, ld_qkv, k_cache, v_cache, lens, parent, counts, B, N, H, Hkv, H / Hkv, D,
-                   Tc, out, ld_out, lse, static_cast<float*>(workspace), device_error_word(), nullptr};
+                   Tc, out, ld_out, lse, static_cast<float*>(workspace), device_error_word(), nullptr,
+                   zero};
     if (!a.err) return GPT2_ERR_CUDA;
     return launch_tree_attn(a, dtype == GPT2_BF16, static_cast<cudaStream_t>(stream));
   } catch (...) {

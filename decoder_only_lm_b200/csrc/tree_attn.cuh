@@ -383,7 +383,19 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   const bool there = r < seq_dims(a, b).n * a.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 seg = a.seg[int64_t(bh) * ceil_div(int(R), MR) + r / MR];
-  if (!there) return;
+  const int i = r / a.G, h = hk * a.G + r % a.G;
+  T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + i) * a.ld_out + int64_t(h) * D + lane * 4;
+  float* lse = a.lse ? a.lse + (int64_t(b) * a.H + h) * a.N + i : nullptr;
+  if (!there) {
+    if (a.zero && (!kWide || group == 0)) {
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+      else
+        *reinterpret_cast<float4*>(out) = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lse && lane == 0) *lse = 0.f;
+    }
+    return;
+  }
   const int np = seg.y - seg.x + 1;  // the first in its CTA's second slot
   if (np == 1) return;               // finished by its CTA
   const int64_t sf = slot_floats<MR>(D);
@@ -424,8 +436,6 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
 #pragma unroll
     for (int g = 1; g < NG; ++g) add(sh_ml[g].x, sh_ml[g].y, sh_o[g * LP + lane]);
   }
-  const int i = r / a.G, h = hk * a.G + r % a.G;
-  T* out = static_cast<T*>(a.out) + (int64_t(b) * a.N + i) * a.ld_out + int64_t(h) * D + lane * 4;
   const float inv = 1.f / l;
   if constexpr (sizeof(T) == 2) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
@@ -435,7 +445,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   } else {
     *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   }
-  if (a.lse && lane == 0) a.lse[(int64_t(b) * a.H + h) * a.N + i] = (M + log2f(l)) * kLn2;
+  if (lse && lane == 0) *lse = (M + log2f(l)) * kLn2;
 }
 
 // Launched with programmatic serialisation: its blocks may be resident before

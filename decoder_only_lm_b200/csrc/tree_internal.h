@@ -39,6 +39,7 @@ struct TreeAttnArgs {
   float* ws;
   int* err;
   int2* seg;  // in the workspace, set by the launchers
+  bool zero;  // rows without a node become 0
 };
 
 size_t tree_attn_workspace(int B, int N, int H, int Hkv, int D, int bf16);

@@ -63,6 +63,8 @@ extern "C" {
 /* element types of op-level buffers */
 #define GPT2_F32 0
 #define GPT2_BF16 1
+/* added to the type of gpt2_tree_attention: rows without a node become 0 */
+#define GPT2_ZERO_ROWS 256
 
 typedef struct gpt2_handle gpt2_handle;
 
@@ -553,12 +555,14 @@ int gpt2_linear(int epi, const void* x, const void* w, int w_kn, const float* bi
  * root, i included [ZERO: Attention; CS336: text generation].  lse (nullable),
  * fp32 [B, H, N]: log of the softmax's normaliser.  The caches are read only up
  * to lens[b] and not written; what other nodes or cache rows hold (infinities
- * and NaN too) does not reach a row.  Rows of nodes i >= counts[b] of out and
- * lse are left as they were.  out: row (b, i) at (b N + i) ld_out, ld_out >=
- * H D; out, lse and workspace overlap nothing else.  fp32 accumulation and softmax; with GPT2_BF16 the probabilities are
- * rounded to bf16 for the product with v.  workspace: device memory of at least
- * gpt2_tree_attention_workspace() bytes, free again when the call's work is
- * done (calls that may overlap need one each).  Results do not depend on
+ * and NaN too) does not reach a row.  Rows of out and lse without a node (i >=
+ * counts[b], and all of a sequence whose length or count is out of range) are
+ * left as they were; with GPT2_ZERO_ROWS added to dtype they become 0.  out: row
+ * (b, i) at (b N + i) ld_out, ld_out >= H D; out, lse and workspace overlap
+ * nothing else.  fp32 accumulation and softmax; with GPT2_BF16 the probabilities
+ * are rounded to bf16 for the product with v.  workspace: device memory of at
+ * least gpt2_tree_attention_workspace() bytes, free again when the call's work
+ * is done (calls that may overlap need one each).  Results do not depend on
  * timing.  Asynchronous on `stream`. */
 int gpt2_tree_attention_workspace(int B, int N, int H, int Hkv, int D, int dtype, size_t* bytes);
 int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, const void* v_cache,

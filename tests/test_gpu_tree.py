@@ -790,3 +790,42 @@ def test_bad_input_is_no_timeout(g):
     assert g.device_error() == g.ERR_ARG
     assert g.device_error() == 0
     gm.close()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,D,B", [(1, 64, 5), (6, 16, 5), (6, 64, 5), (70, 64, 5), (40, 128, 40)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_attention_own_buffers_hold_zeros(g, dtype, N, D, B, ragged):
+    """Rows without a node of the buffers that the call allocates are 0: beyond
+    the counts, and of sequences whose length or count is out of range, also
+    when no counts are given.  One buffer of the caller: its rows stay."""
+    import torch
+    lens = [50, -1, 101, 0, 30] * (B // 5)
+    counts = [N, N, N, max(N - 3, 0), N + 1] * (B // 5) if ragged else None
+    real = [N, 0, 0, max(N - 3, 0), 0] * (B // 5) if ragged else [N, 0, 0, N, N] * (B // 5)
+    c = Case(dtype, B, N, 2, 2, D, 100, lens, seed=3, counts=counts)
+    sizes = (B * N * 2 * D, c.dt), (B * 2 * N, torch.float32)
+
+    def rows(out, lse, value, of_lse):
+        for b in range(B):
+            assert (out[b, real[b]:] == value).all() and (lse[b, :, real[b]:] == of_lse).all()
+
+    # what the allocator gives out next is not 0
+    old = [torch.full((n,), 7.0, dtype=t, device="cuda") for n, t in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    del old
+    out, lse = c.call(g)
+    rows(out, lse, 0, 0)
+    assert g.device_error() == g.ERR_ARG
+    good = [b for b in range(B) if real[b]]
+    whole = c.counts
+    c.counts = np.asarray(real, np.int32)
+    c.check(out, lse, seqs=good)
+    c.counts = whole
+    mine = torch.full((B, N, 2 * D), 7.0, dtype=c.dt, device="cuda")
+    got = c.call(g, out=mine)
+    rows(mine, got[1], 7, 0)
+    got = c.call(g, lse=torch.full((B, 2, N), 7.0, device="cuda"))
+    rows(got[0], got[1], 0, 7)
+    assert g.device_error() == g.ERR_ARG
+    assert g.device_error() == 0

@@ -164,3 +164,13 @@ def test_plain_verify_follows_its_definition():
     assert tree_ref.verify(z, None, tok, par, u, 1.0, 0, 1.0) == ([0], 0)
     u[0] = 0.67
     assert tree_ref.verify(z, None, tok, par, u, 1.0, 0, 1.0) == ([0], 2)
+
+
+def test_tree_attention_takes_zero_rows_with_either_type(g):
+    """GPT2_ZERO_ROWS is added to a type; what is no type stays refused."""
+    for dt in (7 + g.ZERO_ROWS, 2 * g.ZERO_ROWS):
+        assert attention(g, dtype=dt) == g.ERR_ARG
+        assert g.lib.gpt2_last_error(None) == b"tree_attention: bad dtype"
+    for dt in (g.F32, g.BF16):  # (refused for the workspace, the last check)
+        assert attention(g, dtype=dt + g.ZERO_ROWS, wsb=0) == g.ERR_ARG
+        assert b"workspace" in g.lib.gpt2_last_error(None)

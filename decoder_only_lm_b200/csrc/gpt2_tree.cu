@@ -51,7 +51,7 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
   const bool zero = dtype & GPT2_ZERO_ROWS;
   dtype &= ~GPT2_ZERO_ROWS;
   if (!type_ok(dtype)) return refuse("tree_attention: bad dtype");
-  if (!heads_ok(B, N, H, Hkv, D) || Tc < 1 || int64_t(B) * Hkv * Tc > int64_t(0x7FFFFFFF))
+  if (!heads_ok(B, N, H, Hkv, D) || Tc < 1 || int64_t(B) * Hkv * Tc > kTreeMaxRows)
     return refuse("tree_attention: B, N (1..256), H, Hkv, D (16, 32, 64, 128) or Tc out of range");
   if (!row_ok(ld_qkv, dtype, (int64_t(H) + 2 * Hkv) * D) || !row_ok(ld_out, dtype, int64_t(H) * D))
     return refuse("tree_attention: ld_qkv or ld_out too small or not a multiple of 16 bytes");

@@ -60,6 +60,9 @@ struct TreeVerifyArgs {
   int* err;
 };
 constexpr int kTreeMaxNodes = 256;
+// Rows of a cache: tiles of 64 keys are counted and placed in 32 bits, the last one
+// reaching up to 63 behind a length.
+constexpr int64_t kTreeMaxRows = 0x7FFFFFFF - 64;
 constexpr int kTreeMaxVocab = 65536;
 int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st);
 // the same for a temperature above 0 and 1 <= top_k <= kTreeTop, top_k < V

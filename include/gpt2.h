@@ -549,7 +549,8 @@ int gpt2_linear(int epi, const void* x, const void* w, int w_kn, const float* bi
  * Every device pointer 16-byte aligned; ld_qkv a multiple of 16 bytes; D = 16,
  * 32, 64 or 128; H a multiple of Hkv; dtype GPT2_F32 or GPT2_BF16. */
 
-/* Attention of the nodes over the cache (B Hkv Tc < 2^31 rows) and over each other:
+/* Attention of the nodes over the cache (B Hkv Tc <= 2^31 - 65 rows) and over each
+ * other:
  *   out[b, i, hD ..] = sum_j p_j v_j,  p = softmax(q_i . k_j / sqrt(D))
  * over the cached positions j < lens[b] and the nodes on the path from i to the
  * root, i included [ZERO: Attention; CS336: text generation].  lse (nullable),

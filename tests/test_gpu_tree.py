@@ -829,3 +829,19 @@ def test_attention_own_buffers_hold_zeros(g, dtype, N, D, B, ragged):
     rows(got[0], got[1], 0, 7)
     assert g.device_error() == g.ERR_ARG
     assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,N", [("bf16", 40), ("bf16", 70), ("fp32", 5), ("fp32", 60)])
+def test_attention_far_offsets_of_every_kernel(g, dtype, N):
+    """Sequences whose cache rows start past 2^31 elements, in the kernels for
+    more rows and for fp32."""
+    import torch
+    Hkv, Tc, D = 8, 1 << 20, 128
+    c = Case(dtype, 3, N, 8, 8, D, 1, [1, 1, 1], seed=1)
+    c.Tc, c.lens = Tc, np.array([3, 130, 257], np.int32)
+    c.k = torch.empty((3, Hkv, Tc, D), dtype=c.dt, device="cuda")
+    c.v = torch.empty((3, Hkv, Tc, D), dtype=c.dt, device="cuda")
+    c.k[:, :, :300] = torch.randn((3, Hkv, 300, D), device="cuda").to(c.dt)
+    c.v[:, :, :300] = torch.randn((3, Hkv, 300, D), device="cuda").to(c.dt)
+    c.check(*c.call(g))
+    assert g.device_error() == 0

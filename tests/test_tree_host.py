@@ -174,3 +174,12 @@ def test_tree_attention_takes_zero_rows_with_either_type(g):
     for dt in (g.F32, g.BF16):  # (refused for the workspace, the last check)
         assert attention(g, dtype=dt + g.ZERO_ROWS, wsb=0) == g.ERR_ARG
         assert b"workspace" in g.lib.gpt2_last_error(None)
+
+
+def test_tree_attention_limit_of_cache_rows(g):
+    """A length plus a tile has to fit 32 bits: 2^31 - 65 rows of a cache at most."""
+    for kw in (dict(Tc=2 ** 31 - 64), dict(Tc=2 ** 31 - 1), dict(B=2, Tc=2 ** 30 - 32)):
+        assert attention(g, wsb=0, **kw) == g.ERR_ARG
+        assert b"out of range" in g.lib.gpt2_last_error(None)
+    assert attention(g, Tc=2 ** 31 - 65, wsb=0) == g.ERR_ARG
+    assert b"workspace" in g.lib.gpt2_last_error(None)

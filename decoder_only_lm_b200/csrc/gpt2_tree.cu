@@ -19,6 +19,11 @@ int refuse(const char* what) noexcept {
   return GPT2_ERR_ARG;
 }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// n elements of 4 bytes at p share memory with m at q
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + uintptr_t(m) * 4 && b < a + uintptr_t(n) * 4;
+}
 // limits shared by the calls: grid sizes and 32-bit row counts
 bool heads_ok(int B, int N, int H, int Hkv, int D) {
   return B >= 1 && B <= 65535 && N >= 1 && N <= kTreeMaxNodes && Hkv >= 1 && H >= Hkv &&
@@ -98,7 +103,6 @@ int gpt2_kv_append(const void* qkv, int64_t ld_qkv, const int32_t* lens, const i
                    const int32_t* n_path, int dtype, int n_layer, int B, int N, int H, int Hkv,
                    int D, int Tc, void* k_cache, void* v_cache, int32_t* new_lens, void* stream) {
   if (!qkv || !lens || !k_cache || !v_cache) return refuse("kv_append: null pointer");
-  if (new_lens == lens) return refuse("kv_append: new_lens must not be lens");
   if (!type_ok(dtype)) return refuse("kv_append: bad dtype");
   if (!heads_ok(B, N, H, Hkv, D) || Tc < 1 || n_layer < 1 || n_layer > 65535)
     return refuse("kv_append: n_layer, B, N (1..256), H, Hkv, D (16, 32, 64, 128) or Tc out of range");
@@ -106,6 +110,10 @@ int gpt2_kv_append(const void* qkv, int64_t ld_qkv, const int32_t* lens, const i
     return refuse("kv_append: ld_qkv too small or not a multiple of 16 bytes");
   if (!aligned16(qkv) || !aligned16(k_cache) || !aligned16(v_cache))
     return refuse("kv_append: pointers must be 16-byte aligned");
+  // (one block writes them while others have yet to read)
+  if (overlap(new_lens, B, lens, B) || overlap(new_lens, B, n_path, B) ||
+      overlap(new_lens, B, path, int64_t(B) * N))
+    return refuse("kv_append: new_lens must not overlap lens, n_path or path");
   try {
     KvAppendArgs a{qkv, ld_qkv, path, n_path, lens, n_layer, B, N, H, Hkv, D, Tc, k_cache, v_cache,
                    new_lens, device_error_word()};

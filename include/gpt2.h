@@ -609,11 +609,13 @@ int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits,
  * row lens[b] + r of k_cache, v_cache (l-th block of [n_layer, B, Hkv, Tc, D])
  * becomes the k, v part of row path[b N + r] of qkv ([n_layer, B, N] rows,
  * ld_qkv apart).  path NULL: rows 0, 1, ...; n_path NULL: N each.
- * new_lens[b] (nullable, not lens itself) = lens[b] + n_path[b].  Nothing else
- * of the caches is touched; they do not overlap qkv.  A sequence whose rows would not fit (lens[b] < 0,
- * n_path[b] outside 0 .. N, or lens[b] + n_path[b] > Tc) is left as it is, its
- * new_lens[b] = lens[b]; a node index outside [0, N) is skipped; both are
- * recorded for gpt2_device_error (GPT2_ERR_ARG). */
+ * new_lens[b] (nullable) = lens[b] + n_path[b].  Nothing else of the caches is
+ * touched; they do not overlap qkv, and new_lens overlaps nothing else.  A
+ * sequence whose rows would not fit (lens[b] < 0, n_path[b] outside 0 .. N, or
+ * lens[b] + n_path[b] > Tc) is left as it is, its new_lens[b] = lens[b]; a node
+ * index outside [0, N) is skipped; both are recorded for gpt2_device_error
+ * (GPT2_ERR_ARG).  GPT2_ERR_ARG at once if new_lens overlaps lens, n_path or
+ * path. */
 int gpt2_kv_append(const void* qkv, int64_t ld_qkv, const int32_t* lens, const int32_t* path,
                    const int32_t* n_path, int dtype, int n_layer, int B, int N, int H, int Hkv,
                    int D, int Tc, void* k_cache, void* v_cache, int32_t* new_lens, void* stream);

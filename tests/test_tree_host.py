@@ -79,6 +79,15 @@ def test_kv_append_refuses(g, bad):
     assert rc == g.ERR_ARG and b"kv_append" in g.lib.gpt2_last_error(None)
 
 
+@pytest.mark.parametrize("new", [8192, 8188, 8200, 12288, 12296, 12284, 16384, 16384 + 44, 16380])
+def test_kv_append_refuses_lengths_over_its_inputs(g, new):
+    """new_lens may not overlap lens, n_path or path, which other blocks read."""
+    V = C.c_void_p
+    rc = g.lib.gpt2_kv_append(P, 192, V(8192), V(16384), V(12288), g.BF16, 1, 3, 4, 1, 1, 64, 16, P, P,
+                              V(new), None)
+    assert rc == g.ERR_ARG and b"new_lens" in g.lib.gpt2_last_error(None)
+
+
 def test_binding_checks_cpu_tensors(g):
     """Tensors that are not on a GPU, or do not fit together, are refused before
     any library call."""

@@ -20,9 +20,9 @@ int refuse(const char* what) noexcept {
 }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 // n elements of 4 bytes at p share memory with m at q
-bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
   const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + uintptr_t(m) * 4 && b < a + uintptr_t(n) * 4;
+  return p && q && a < b + m * 4 && b < a + n * 4;
 }
 // limits shared by the calls: grid sizes and 32-bit row counts
 bool heads_ok(int B, int N, int H, int Hkv, int D) {
@@ -89,6 +89,16 @@ int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits,
   if (!(temperature >= 0.f && temperature <= 1e20f) || top_k < 0 ||
       !(top_p > 0.f && top_p <= 1.f))
     return refuse("tree_verify: bad sampling settings");
+  // (a sequence's CTAs read while one of them writes)
+  const uint64_t nodes = uint64_t(B) * N, rows = nodes - 1;
+  const struct { const void* p; uint64_t n; } bufs[] = {
+      {path, nodes}, {n_path, uint64_t(B)}, {next, uint64_t(B)}, {logits, rows * uint64_t(ld) + V},
+      {draft_logits, rows * uint64_t(ld_draft) + V}, {tokens, nodes}, {parent, nodes}, {counts, uint64_t(B)},
+      {uniform, nodes}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 9; ++j)
+      if (overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n))
+        return refuse("tree_verify: path, n_path and next must not overlap anything");
   try {
     TreeVerifyArgs a{logits, ld, draft_logits, ld_draft, tokens, parent, counts, uniform, B, N, V,
                      temperature, top_k, top_p, path, n_path, next, device_error_word()};
@@ -112,7 +122,7 @@ int gpt2_kv_append(const void* qkv, int64_t ld_qkv, const int32_t* lens, const i
     return refuse("kv_append: pointers must be 16-byte aligned");
   // (one block writes them while others have yet to read)
   if (overlap(new_lens, B, lens, B) || overlap(new_lens, B, n_path, B) ||
-      overlap(new_lens, B, path, int64_t(B) * N))
+      overlap(new_lens, B, path, uint64_t(B) * N))
     return refuse("kv_append: new_lens must not overlap lens, n_path or path");
   try {
     KvAppendArgs a{qkv, ld_qkv, path, n_path, lens, n_layer, B, N, H, Hkv, D, Tc, k_cache, v_cache,

@@ -595,8 +595,8 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
  * draft row, or are distinct guesses.
  * path[b N + r] = the accepted nodes in order, node 0 first, -1 behind them;
  * n_path[b] their number (>= 1); counts[b] = 0 gives n_path 0 and next -1.
- * A token outside [0, V) is never accepted.  A node with parent -1 other than
- * the root is never reached.  All integers exact and deterministic.
+ * path, n_path and next overlap nothing else.  A token outside [0, V) is never
+ * accepted.  A node with parent -1 other than the root is never reached.  All integers exact and deterministic.
  * GPT2_ERR_ARG unless 1 <= V <= 65536, V <= ld (and ld_draft), 0 <= temperature
  * <= 1e20, top_k >= 0, 0 < top_p <= 1, 1 <= N <= 256. */
 int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits, int64_t ld_draft,

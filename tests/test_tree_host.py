@@ -65,6 +65,26 @@ def test_tree_verify_refuses(g, bad):
     assert rc == g.ERR_ARG and b"tree_verify" in g.lib.gpt2_last_error(None)
 
 
+VERIFY_BUFFERS = ["logits", "draft", "tokens", "parent", "counts", "uniform", "path", "n", "next"]
+
+
+@pytest.mark.parametrize("which,over", [(a, b) for a in ("path", "n", "next") for b in VERIFY_BUFFERS
+                                        if a != b])
+def test_tree_verify_refuses_outputs_over_its_arguments(g, which, over):
+    """The CTAs of a sequence read while one of them writes: an output may not
+    share memory with an input or another output."""
+    at = {n: 1 << (20 + i) for i, n in enumerate(VERIFY_BUFFERS)}
+    last = {"logits": 8 * 100 * 4, "draft": 8 * 100 * 4, "counts": 8, "n": 8, "next": 8}.get(over, 32) - 4
+    for offset in (0, last):  # the first and the last element
+        a = dict(at)
+        a[which] = at[over] + offset
+        a = {k: C.c_void_p(v) for k, v in a.items()}
+        rc = g.lib.gpt2_tree_verify(a["logits"], 100, a["draft"], 100, a["tokens"], a["parent"],
+                                    a["counts"], a["uniform"], 2, 4, 100, 1.0, 0, 1.0, a["path"],
+                                    a["n"], a["next"], None)
+        assert rc == g.ERR_ARG and b"tree_verify" in g.lib.gpt2_last_error(None)
+
+
 @pytest.mark.parametrize("bad", [
     dict(qkv=None), dict(lens=None), dict(k=None), dict(v=None), dict(new=C.c_void_p(8192)),
     dict(dtype=3), dict(L=0), dict(L=65536), dict(B=0), dict(N=257), dict(D=20), dict(Tc=0),

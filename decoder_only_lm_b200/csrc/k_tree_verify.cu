@@ -8,10 +8,10 @@
 // draw from max(0, p - q), which together gives a draw from p.
 //
 // Weights.  A row z of logits stands for the integers
-//   w_i = rint(2^36 exp((z_i - max z) / temperature))      (64-bit exp)
-// with the ids outside the top-k and top-p cuts set to 0 (ids ordered by logit,
-// the smaller id first among equal ones).  Sums of integers do not depend on
-// their order, so every decision below is exact and repeatable.  With S the sum
+//   w_i = 2^36 exp((z_i - max z) / temperature)      (64-bit exp, see Exp)
+// as whole numbers, the ids outside the top-k and top-p cuts set to 0 (ids ordered
+// by logit, the smaller id first among equal ones).  Sums of integers do not
+// depend on their order, so every decision below is repeatable.  With S the sum
 // of the target's weights, x the draft's weights and X their sum, at the node
 // that the walk stands at, for its children c in id order:
 //   accept  iff  u_c x_c S / X < w_c   (draft given)   or   u_c S < w_c

@@ -34,9 +34,11 @@ __device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z;
 // (P. Tang's scheme, 1989).  With x = 64 d log2(e) / T = r - n, n the nearest
 // integer (from the 1.5 * 2^52 shift): 2^36 exp(-d / T) = 2^(36 + n / 64) 2^(r / 64),
 // the first factor from a table of 64 and an exponent, the second from its Taylor
-// sum, |r ln2 / 64| < 0.0055: the first term left out is below 4e-17.  A weight is
-// within 2^-14 of the value it rounds.  Returned as 2^52 + weight, whose low 52
-// bits are the integer.
+// sum, |r ln2 / 64| < 0.0055: the first term left out is below 4e-17.  What is
+// rounded is within 2^-14 of 2^36 exp(-d / T) (below 2^-16 in 40000 arguments
+// computed in 60 digits), so a weight is the nearest whole number except, rarely,
+// next to the middle of two.  Returned as 2^52 + weight, whose low 52 bits are the
+// integer.
 constexpr double kOnes = 4503599627370496.0;  // 2^52
 struct Exp {
   const double* table;  // 2^(36 + i / 64)

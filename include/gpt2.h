@@ -579,9 +579,11 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
  * the one its children were drawn from; NULL: the children are guesses without
  * a distribution.  Both are taken at the given temperature, top-k and top-p,
  * with the meaning of gpt2_sample except that exp is evaluated in 64 bits and
- * ids are ordered by logit: w_i = rint(2^36 exp((z_i - max z) / temperature))
- * over the first V columns, 0 outside the cuts; NaN counts as -infinity;
- * temperature 0 keeps the highest logit alone (the smaller id on ties).
+ * ids are ordered by logit: w_i is 2^36 exp((z_i - max z) / temperature) as a
+ * whole number (the nearest; within 2^-14 of the middle of two it may be the
+ * other one) over the first V columns, 0 outside the cuts; NaN counts as
+ * -infinity; temperature 0 keeps the highest logit alone (the smaller id on
+ * ties).
  * From cur = 0, with S = sum w of cur's row and X = sum x of its draft row, for
  * the children c of cur in increasing order, t = tokens[b N + c]:
  *   accept c (cur = c) if u_c x_t S / X < w_t   (no draft: u_c S < w_t),
@@ -592,11 +594,12 @@ int gpt2_tree_attention(const void* qkv, int64_t ld_qkv, const void* k_cache, co
  * [0, 1), clamped; every node its own number, the root's serves the draw).
  * Drawn that way, the accepted tokens and next[b] have the target's
  * distribution when the children of a node are drawn independently from its
- * draft row, or are distinct guesses.
+ * draft row, at the same temperature, top-k and top-p, or are distinct guesses.
  * path[b N + r] = the accepted nodes in order, node 0 first, -1 behind them;
  * n_path[b] their number (>= 1); counts[b] = 0 gives n_path 0 and next -1.
  * path, n_path and next overlap nothing else.  A token outside [0, V) is never
- * accepted.  A node with parent -1 other than the root is never reached.  All integers exact and deterministic.
+ * accepted.  A node with parent -1 other than the root is never reached.  Sums
+ * of weights are exact, so results do not depend on timing.
  * GPT2_ERR_ARG unless 1 <= V <= 65536, V <= ld (and ld_draft), 0 <= temperature
  * <= 1e20, top_k >= 0, 0 < top_p <= 1, 1 <= N <= 256. */
 int gpt2_tree_verify(const float* logits, int64_t ld, const float* draft_logits, int64_t ld_draft,

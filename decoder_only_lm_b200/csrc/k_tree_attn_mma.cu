@@ -270,91 +270,92 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
         if (!ok) break;
       }
       if (busy && nw > 0) {
-      // scores
-      float sc[NT][4];
+        // scores
+        float sc[NT][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-        const int r = wk * KW + j * 8 + (lane & 7);
-        if (KS >= 2) {
+        for (int j = 0; j < NT; ++j) {
+          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+          const int r = wk * KW + j * 8 + (lane & 7);
+          if (KS >= 2) {
 #pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            uint32_t kb[4];
-            ldm4(kb, sk + at<D>(r, 2 * k + (lane >> 3)));
-            mma16816(sc[j], q[k], kb[0], kb[1]);
-            mma16816(sc[j], q[(k + 1) % KS], kb[2], kb[3]);
+            for (int k = 0; k < KS; k += 2) {
+              uint32_t kb[4];
+              ldm4(kb, sk + at<D>(r, 2 * k + (lane >> 3)));
+              mma16816(sc[j], q[k], kb[0], kb[1]);
+              mma16816(sc[j], q[(k + 1) % KS], kb[2], kb[3]);
+            }
           }
         }
-      }
-      if (KS == 1) {  // D = 16: one step, two key tiles a load
+        if (KS == 1) {  // D = 16: one step, two key tiles a load
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          uint32_t kb[4];
-          ldm4(kb, sk + at<D>(wk * KW + j * 8 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
-          mma16816(sc[j], q[0], kb[0], kb[1]);
-          mma16816(sc[j + 1], q[0], kb[2], kb[3]);
+          for (int j = 0; j < NT; j += 2) {
+            uint32_t kb[4];
+            const int r = wk * KW + j * 8 + (lane & 7) + ((lane >> 4) << 3);
+            ldm4(kb, sk + at<D>(r, (lane >> 3) & 1));
+            mma16816(sc[j], q[0], kb[0], kb[1]);
+            mma16816(sc[j + 1], q[0], kb[2], kb[3]);
+          }
         }
-      }
-      if (fresh || nw < KW) {
-        uint64_t see[2] = {~uint64_t(0), ~uint64_t(0)};
-        if (fresh) {
-          see[0] = sees(!a.parent, mask, node[0], k0) >> (wk * KW);
-          see[1] = sees(!a.parent, mask, node[1], k0) >> (wk * KW);
+        if (fresh || nw < KW) {
+          uint64_t see[2] = {~uint64_t(0), ~uint64_t(0)};
+          if (fresh) {
+            see[0] = sees(!a.parent, mask, node[0], k0) >> (wk * KW);
+            see[1] = sees(!a.parent, mask, node[1], k0) >> (wk * KW);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = j * 8 + gc * 2 + (e & 1);
+              if (key >= nw || !((see[e >> 1] >> key) & 1)) sc[j][e] = -INFINITY;
+            }
+        }
+        // running maximum (log2 domain: s scale), probabilities, sums
+        float base[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = m[h];
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mx = fmaxf(mx, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // a row that has seen nothing yet: every p is 2^(-inf) = 0
+          // (products rounded, not fused: an unchanged maximum gives alpha = 1)
+          base[h] = mx == -INFINITY ? 0.f : __fmul_rn(mx, scale);
+          const float alpha = ex2(__fmul_rn(m[h], scale) - base[h]);
+          m[h] = mx;
+          l[h] *= alpha;
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < DT; ++j) {
+              o[j][2 * h] *= alpha;
+              o[j][2 * h + 1] *= alpha;
+            }
+          }
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = j * 8 + gc * 2 + (e & 1);
-            if (key >= nw || !((see[e >> 1] >> key) & 1)) sc[j][e] = -INFINITY;
+            sc[j][e] = ex2(fmaf(sc[j][e], scale, -base[e >> 1]));
+            l[e >> 1] += sc[j][e];
           }
-      }
-      // running maximum (log2 domain: s scale), probabilities, sums
-      float base[2];
+        // O += P V
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = m[h];
+        for (int k = 0; k < NT / 2; ++k) {
+          uint32_t pr[4] = {pack2(sc[2 * k][0], sc[2 * k][1]), pack2(sc[2 * k][2], sc[2 * k][3]),
+                           pack2(sc[2 * k + 1][0], sc[2 * k + 1][1]),
+                           pack2(sc[2 * k + 1][2], sc[2 * k + 1][3])};
+          const int r = wk * KW + k * 16 + (lane & 15);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          mx = fmaxf(mx, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // a row that has seen nothing yet: every p is 2^(-inf) = 0
-        // (products rounded, not fused: an unchanged maximum gives alpha = 1)
-        base[h] = mx == -INFINITY ? 0.f : __fmul_rn(mx, scale);
-        const float alpha = ex2(__fmul_rn(m[h], scale) - base[h]);
-        m[h] = mx;
-        l[h] *= alpha;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-          for (int j = 0; j < DT; ++j) {
-            o[j][2 * h] *= alpha;
-            o[j][2 * h + 1] *= alpha;
+          for (int j = 0; j < DT; j += 2) {
+            uint32_t vb[4];
+            ldm4_trans(vb, sv + at<D>(r, j + (lane >> 4)));
+            mma16816(o[j], pr, vb[0], vb[1]);
+            mma16816(o[j + 1], pr, vb[2], vb[3]);
           }
         }
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[j][e] = ex2(fmaf(sc[j][e], scale, -base[e >> 1]));
-          l[e >> 1] += sc[j][e];
-        }
-      // O += P V
-#pragma unroll
-      for (int k = 0; k < NT / 2; ++k) {
-        uint32_t pr[4] = {pack2(sc[2 * k][0], sc[2 * k][1]), pack2(sc[2 * k][2], sc[2 * k][3]),
-                         pack2(sc[2 * k + 1][0], sc[2 * k + 1][1]),
-                         pack2(sc[2 * k + 1][2], sc[2 * k + 1][3])};
-        const int r = wk * KW + k * 16 + (lane & 15);
-#pragma unroll
-        for (int j = 0; j < DT; j += 2) {
-          uint32_t vb[4];
-          ldm4_trans(vb, sv + at<D>(r, j + (lane >> 4)));
-          mma16816(o[j], pr, vb[0], vb[1]);
-          mma16816(o[j + 1], pr, vb[2], vb[3]);
-        }
-      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(b_empty(s));
@@ -473,7 +474,7 @@ struct Variant {
       return GPT2_ERR_CUDA;
     }
     static std::atomic<uint64_t> allowed{0};
-  GPT2_CUDA_TRY(allow_smem(allowed, tree_attn_mma_kernel<D, WM, WK>, F::kSmem));
+    GPT2_CUDA_TRY(allow_smem(allowed, tree_attn_mma_kernel<D, WM, WK>, F::kSmem));
     const TreeAttnArgs w = with_workspace<F::MR>(a, grid());
     tree_attn_mma_kernel<D, WM, WK><<<grid(), F::kThreads, F::kSmem, st>>>(mk, mv, mx, w);
     COUNT_LAUNCH(1);

@@ -133,7 +133,8 @@ __device__ void share_nonfinite(const TreeAttnArgs& a, const Piece& p, int hq, i
     constexpr int kCols = D / P;  // columns of a copy
     static_assert(kCols <= 64, "a bit for each column");
     auto column = [&](int i) { return 16 * (copy + P * (i / 16)) + i % 16; };
-    const bf16* q = static_cast<const bf16*>(a.qkv) + (int64_t(p.b) * a.N + node) * a.ld_qkv + int64_t(hq) * D;
+    const bf16* q = static_cast<const bf16*>(a.qkv) + (int64_t(p.b) * a.N + node) * a.ld_qkv +
+                    int64_t(hq) * D;
     const int64_t row0 = (int64_t(p.b) * a.Hkv + p.hk) * a.Tc;
     const bf16* kc = static_cast<const bf16*>(a.k) + row0 * D;
     const bf16* vc = static_cast<const bf16*>(a.v) + row0 * D;
@@ -177,9 +178,9 @@ __device__ __noinline__ void share_nonfinite(const TreeAttnArgs& a, const Listed
   const bool mine = row < p.rows;
   const int gr = p.rt * MR + (mine ? row : 0), node = gr / a.G, hq = p.hk * a.G + gr % a.G;
   if (p.whole())
-    share_nonfinite<D, P>(a, p, hq, node, mine, any_bad, bad, mask, m, 1.f / l,
-                          static_cast<bf16*>(a.out) + (int64_t(p.b) * a.N + node) * a.ld_out + int64_t(hq) * D,
-                          copy);
+    share_nonfinite<D, P>(
+        a, p, hq, node, mine, any_bad, bad, mask, m, 1.f / l,
+        static_cast<bf16*>(a.out) + (int64_t(p.b) * a.N + node) * a.ld_out + int64_t(hq) * D, copy);
   else
     share_nonfinite<D, P>(a, p, hq, node, mine, any_bad, bad, mask, m, 1.f,
                           a.ws + p.slot * slot_floats<MR>(D) + int64_t(row) * D, copy);

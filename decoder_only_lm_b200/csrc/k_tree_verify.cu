@@ -759,8 +759,8 @@ int launch(const TreeVerifyArgs& a, cudaStream_t st) {
 
 int launch_tree_verify(const TreeVerifyArgs& a, cudaStream_t st) {
   const bool top = a.temperature > 0.f && a.top_k > 0 && a.top_k < a.V;
-  // the kept ids as a list, as long as they fit (3 to 4 times as fast as the
-  // histogram wherever both were measured: its figures stand with it)
+  // the kept ids as a list, as long as they fit (2.7 to 4.3 times as fast as the
+  // histogram where both were measured: the figures stand with the list's kernel)
   if (top && a.top_k <= kTreeTop) return launch_tree_verify_top(a, st);
   const bool cuts = top || (a.temperature > 0.f && a.top_p < 1.f);
   if (a.draft) return cuts ? launch<true, true>(a, st) : launch<true, false>(a, st);

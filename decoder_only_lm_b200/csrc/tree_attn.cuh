@@ -9,11 +9,12 @@
 // order, form one list, and every CTA takes an equal run of it, whatever the
 // lengths are: a long sequence is split over many CTAs, short ones share one.
 // Each segment counts kExtra tiles more than it has, for what a piece costs
-// besides its tiles (queries, masks, results; each kernel has its own number).  Lengths are read on the device, so a recorded launch follows
-// them.  A segment inside one CTA's run is finished there; the pieces of any
-// other go to the workspace (unnormalised output, running maximum and sum in
-// fp32) and tree_combine_kernel merges them in tile order, so the result does
-// not depend on timing.
+// besides its tiles (queries, masks, results; each kernel has its own number).
+// Lengths are read on the device, so a recorded launch follows them.  A segment
+// inside one CTA's run is finished there; the pieces of any other go to the
+// workspace (unnormalised output, running maximum and sum in fp32) and
+// tree_combine_kernel merges them in tile order, so the result does not depend on
+// timing.
 #pragma once
 
 #include "kernels.h"

@@ -14,8 +14,8 @@
 // next tile's keys during a tile's product with V, its values during the next
 // scores, so two buffers do for the overlap (B200, 16 single tokens over 500-2000
 // positions, 12 heads of 64: 48 -> 35 us, 3.5 TB/s; trees of 13 over up to 1000,
-// 4 sequences: 16 us; trees of 64 over up to 2000, 8 sequences: 77 us, 17 TFLOP/s,
-// bound by shared memory reads).
+// 4 sequences: 14 us; trees of up to 64 over 500-2000, 8 sequences: 83 us, 18
+// TFLOP/s, bound by shared memory reads).
 
 #include <type_traits>
 

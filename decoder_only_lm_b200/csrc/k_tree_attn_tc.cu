@@ -33,9 +33,9 @@
 //
 // What bounds it: with few rows a head the cache's bytes (B200, 4 trees of 48 over
 // 9-33 thousand positions, 12 heads of 64: 52 us, 4.9 TB/s), with full tiles the
-// softmax (8 trees of 64 over 1000-8191, 32 heads on 8 of 128: 65 us), and in short
-// calls the start, a piece's end and the merge (16 trees of 64 over 100-1024, 16
-// heads of 64: 27 us).
+// softmax and the wait for scores (8 trees of 64 over 1000-8191, 32 heads on 8 of
+// 128: 62 us), and in short calls the start, a piece's end and the merge (16 trees
+// of 64 over 100-1024, 16 heads of 64: 25 us).
 //
 // Every wait is bounded (2 s) and reports a timeout in the error word.
 

@@ -12,8 +12,8 @@
 // logit, and with ids dealt out to the groups few others reach it (50257 normal
 // logits: 56 do for k = 50, 253 for k = 200).
 //
-// One cluster of 8 CTAs per sequence.  What bounds it is the latency of the walk;
-// a node takes three exchanges over the cluster: of the groups' maxima, of the ids
+// One cluster of 8 CTAs per sequence (33 run at a time).  What bounds it is the
+// latency of the walk; a node takes three exchanges over the cluster: of the groups' maxima, of the ids
 // that reach the bound, and of each one's place among them, which the CTA that it
 // came from counts.  Behind them every CTA holds the list in order, and accepting,
 // rejecting, taking the draft's weights off and the draw need no other CTA.  A row's

@@ -1358,22 +1358,6 @@ bool make_map_bf16(CUtensorMap* map, const void* base, int64_t inner, int64_t ou
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
-bool make_map_rows(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld,
-                   int box_inner, int box_outer) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
-  cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
-  cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_outer)};
-  cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapSwizzle swizzle = box_inner == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : box_inner == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
 bool make_map_epi(CUtensorMap* map, const void* base, int elem_bytes, int64_t inner,
                   int64_t outer, int64_t ld) {
   EncodeTiledFn fn = encode_fn();

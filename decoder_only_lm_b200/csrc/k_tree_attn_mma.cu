@@ -460,6 +460,31 @@ __global__ void __launch_bounds__(Cfg<D, WM, WK>::kThreads, Cfg<D, WM, WK>::kCta
   }
 }
 
+// Tensor map over row-major [outer, inner] bf16 with row stride ld (elements), box
+// {box_inner, KT}, box_inner 64, 32 or 16 elements and the swizzle of its width
+// (128, 64 or 32 bytes), zero fill out of range.
+bool make_map_rows(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld,
+                   int box_inner) {
+  static const auto encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(
+        e == cudaSuccess && q == cudaDriverEntryPointSuccess ? p : nullptr);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
+  const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(KT)};
+  const cuuint32_t step[2] = {1, 1};
+  const CUtensorMapSwizzle swizzle = box_inner == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : box_inner == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+                step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int WM, int WK>
 struct Variant {
   using F = Cfg<D, WM, WK>;
@@ -468,8 +493,8 @@ struct Variant {
     CUtensorMap mk, mv, mx;
     const int64_t rows = int64_t(a.B) * a.Hkv * a.Tc;
     constexpr int box = D < 64 ? D : 64;
-    if (!make_map_rows(&mk, a.k, D, rows, D, box, KT) || !make_map_rows(&mv, a.v, D, rows, D, box, KT) ||
-        !make_map_rows(&mx, a.qkv, int64_t(a.H + 2 * a.Hkv) * D, int64_t(a.B) * a.N, a.ld_qkv, box, KT)) {
+    if (!make_map_rows(&mk, a.k, D, rows, D, box) || !make_map_rows(&mv, a.v, D, rows, D, box) ||
+        !make_map_rows(&mx, a.qkv, int64_t(a.H + 2 * a.Hkv) * D, int64_t(a.B) * a.N, a.ld_qkv, box)) {
       gpt2_internal::set_error("tree_attention: tensor map encoding failed");
       return GPT2_ERR_CUDA;
     }

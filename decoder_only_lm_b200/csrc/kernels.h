@@ -179,6 +179,5 @@ int lmhead_bwd(const void* h, const void* W, const int32_t* y, const float* lse,
                size_t ws_bytes, cudaStream_t st, const LmSide* side = nullptr);
 bool gemm_tc_supported(const GemmArgs& g);
 
-// device error word of the op-level calls (bounded waits); behind it the word of
-// device-side contents out of range
+// device error word of the op-level calls (bounded waits)
 int* device_error_word();

@@ -427,10 +427,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 // (elements), box {64, box_outer}, 128-byte swizzle, zero fill out of range.
 bool make_map_bf16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld,
                    int box_outer);
-// The same with box {box_inner, box_outer}, box_inner 64, 32 or 16 elements and
-// the swizzle of its width (128, 64 or 32 bytes).
-bool make_map_rows(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t ld,
-                   int box_inner, int box_outer);
 // 2-D tensor map for GEMM epilogue chunks: row-major [outer, inner] of bf16
 // (elem_bytes 2) or fp32 (4), row stride ld elements, box {64 B of inner, 128}
 // rows, 64-byte swizzle.

@@ -147,8 +147,13 @@ __device__ void share_nonfinite(const TreeAttnArgs& a, const Piece& p, int hq, i
     const int k1 = p.t1 <= p.ct ? min(p.len, p.t1 * KT) : p.len;
     for (int j0 = __any_sync(0xffffffffu, odd != 0) ? p.t0 * KT : k1; j0 < k1; j0 += 32) {
       bool hit = false;
-      if (const int j = j0 + int(threadIdx.x) % 32; j < k1)
-        for (int i = 0; i < kCols; ++i) hit |= !finite(vc[int64_t(j) * D + column(i)]);
+      if (const int j = j0 + int(threadIdx.x) % 32; j < k1) {
+#pragma unroll
+        for (int i = 0; i < kCols; i += 8) {
+          uint4 u = *reinterpret_cast<const uint4*>(vc + int64_t(j) * D + column(i));
+          hit |= drop_nonfinite(u);
+        }
+      }
       for (unsigned which = __ballot_sync(0xffffffffu, hit); which; which &= which - 1) {
         const int64_t at = (j0 + int64_t(__ffs(int(which)) - 1)) * D;
         if (!odd) continue;

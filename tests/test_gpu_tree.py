@@ -845,3 +845,48 @@ def test_attention_far_offsets_of_every_kernel(g, dtype, N):
     c.v[:, :, :300] = torch.randn((3, Hkv, 300, D), device="cuda").to(c.dt)
     c.check(*c.call(g))
     assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("N", [1, 20, 48, 80])
+def test_attention_infinite_keys(g, dtype, D, N):
+    """An infinite key that every node sees: a score of -inf leaves its key out,
+    one of +inf makes the row NaN, and other rows do not notice."""
+    c = Case(dtype, 2, N, 4, 2, D, 700, [700, 90], seed=D + N)
+    q = c.qkv[..., :c.H * D].view(2, N, c.H, D)
+    q[..., 0] = 1 + q[..., 0].abs()
+    q[:, ::2, :, 0] *= -1
+    for b, key in ((0, 5), (0, 355), (1, 70)):
+        c.k[b, :, key] = 0
+        c.k[b, :, key, 0] = 1e30  # (far below all others for the rows with q < 0)
+    out, lse = [t.clone() for t in c.call(g)]
+    for b, key in ((0, 5), (0, 355), (1, 70)):
+        c.k[b, :, key, 0] = float("inf")
+    got, got_lse = c.call(g)
+    want, want_lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    want[:, 1::2], want_lse[:, :, 1::2] = np.nan, np.nan
+    np.testing.assert_array_equal(got.float().cpu().numpy(), want)
+    np.testing.assert_array_equal(got_lse.cpu().numpy(), want_lse)
+    assert g.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,N", [("fp32", 7), ("bf16", 7), ("bf16", 64)])
+def test_attention_recorded_with_own_buffers(g, dtype, N):
+    """A recorded call that allocates its buffers: rows that have no node at a
+    replay are 0, whatever an earlier one left there."""
+    import torch
+    c = Case(dtype, 4, N, 4, 4, 64, 300, [10, 300, 0, 64], seed=5, counts=[N] * 4)
+    c.call(g)
+    lens, counts, par = cuda(c.lens), cuda(c.counts), cuda(c.par)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = g.tree_attention(c.qkv, c.k, c.v, lens, 4, parent=par, counts=counts)
+    for now in ([N] * 4, [1, 0, N, N - 2], [0] * 4, [N, 2, 1, 0]):
+        c.counts = np.asarray(now, np.int32)
+        counts.copy_(cuda(c.counts))
+        graph.replay()
+        c.check(out, lse)
+        for b in range(4):
+            assert (out[b, now[b]:] == 0).all() and (lse[b, :, now[b]:] == 0).all()
+    assert g.device_error() == 0
